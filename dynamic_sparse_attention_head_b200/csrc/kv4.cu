@@ -1,0 +1,537 @@
+// The paged 4-bit cache: block tables and slot maps from request lengths, release, the quantising
+// write and the read back.  The format is msa_kv4_cache's.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "kernels.h"
+#include "kv4.cuh"
+#include "msa_internal.h"
+
+namespace msa {
+
+msa_status kv4_view(const msa_kv4_cache* c, Kv4View* v) {
+  if (!c || !c->pages || !c->state || c->n_pages < 1 || c->n_pages > 0x7fffffff) return MSA_ERR_INVALID_ARG;
+  const size_t bytes = msa_kv4_page_bytes(c->page_tokens, c->group);
+  if (!bytes || c->Hkv < 1 || c->Hkv > 1024) return MSA_ERR_SHAPE;
+  if ((reinterpret_cast<uintptr_t>(c->pages) | reinterpret_cast<uintptr_t>(c->state)) & 15) return MSA_ERR_ALIGN;
+  v->pages = static_cast<uint8_t*>(c->pages);
+  v->n_pages = c->n_pages;
+  v->page_shift = 0;
+  while ((1 << v->page_shift) < c->page_tokens) ++v->page_shift;
+  v->Hkv = c->Hkv;
+  v->page_bytes = (int64_t)bytes;
+  v->state = static_cast<uint32_t*>(c->state);
+  return MSA_OK;
+}
+
+namespace {
+
+// ---------------------------------------------------------------------------------------
+// slot maps
+// ---------------------------------------------------------------------------------------
+constexpr int SLOT_THREADS = 512;
+
+// Inclusive scan of one value per thread over the block (every thread calls); `sums`: one per warp.
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t s = lane < (int)(blockDim.x >> 5) ? sums[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    sums[lane] = s;
+  }
+  __syncthreads();
+  if (warp) x += sums[warp - 1];
+  __syncthreads();  // `sums` is free again
+  return x;
+}
+
+// Largest b in [0, n) with cum[b] <= x (cum ascending, cum[0] = 0).
+__device__ __forceinline__ int find_last(const int32_t* cum, int n, int32_t x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (cum[m] <= x) lo = m;
+    else hi = m;
+  }
+  return lo;
+}
+
+struct SlotArgs {
+  Kv4View c;
+  const int32_t *kv_lens, *new_lens, *free_pages, *n_free;
+  int32_t *block_table, *kv_out, *n_free_out, *cu_new, *positions;
+  int64_t* slots;
+  int64_t table_stride, capacity;
+  int32_t B, max_blocks;
+};
+
+// Every block scans the lengths for itself (B ints, one or a few per thread) and then takes its
+// share of the tokens and of the new pages by a search in the two running sums; nothing is passed
+// between blocks.  kv_lens_out and n_free_out may be the inputs: they are written by the block
+// that arrives last, when every block has read them.  Bound by launch latency for a decode batch;
+// for prompts by the 12 bytes written per token.
+__global__ void __launch_bounds__(SLOT_THREADS) kv4_slots_kernel(const SlotArgs a) {
+  extern __shared__ int32_t sm[];
+  int32_t* cum_new = sm;                      // [B + 1]
+  int32_t* cum_page = cum_new + a.B + 1;      // [B + 1]: pages wanted by the requests before b
+  int32_t* kv = cum_page + a.B + 1;           // [B]
+  __shared__ int64_t sums[32];
+  __shared__ int last, bad;
+  const int P = a.c.page_shift;
+  if (threadIdx.x == 0) bad = 0;
+  __syncthreads();
+  int64_t n_free = *a.n_free;
+  if (n_free < 0 || n_free > a.c.n_pages) {
+    if (threadIdx.x == 0) bad = 1;
+    n_free = n_free < 0 ? 0 : a.c.n_pages;
+  }
+  int64_t run_new = 0, run_page = 0;
+  for (int b0 = 0; b0 < a.B; b0 += SLOT_THREADS) {
+    const int b = b0 + threadIdx.x;
+    int64_t n = 0, pages = 0;
+    if (b < a.B) {
+      const int64_t have = a.kv_lens[b];
+      n = a.new_lens[b];
+      if (have < 0 || n < 0) bad = 1;
+      if (n < 0) n = 0;
+      kv[b] = (int32_t)have;
+      if (have >= 0) {
+        const int64_t need = (have + n + (1 << P) - 1) >> P;
+        if (need > a.max_blocks) {
+          bad = 1;
+          pages = -1;
+        } else {
+          pages = need - ((have + (1 << P) - 1) >> P);
+        }
+      } else {
+        pages = -1;
+      }
+    }
+    // a request that fits no row is marked by the sign of its length and wants no page
+    const bool refused = pages < 0;
+    const int64_t cn = block_scan(n, sums) + run_new, cp = block_scan(refused ? 0 : pages, sums) + run_page;
+    if (b < a.B) {
+      if (cn > 0x7fffffff || cp > 0x7fffffff) bad = 1;
+      cum_new[b + 1] = (int32_t)min(cn, (int64_t)0x7fffffff);
+      cum_page[b + 1] = (int32_t)min(cp, (int64_t)0x7fffffff);
+      if (refused) kv[b] = kv[b] | (int32_t)0x80000000;
+    }
+    if (threadIdx.x == SLOT_THREADS - 1) sums[31] = cn, sums[30] = cp;
+    __syncthreads();
+    run_new = sums[31];
+    run_page = sums[30];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    cum_new[0] = cum_page[0] = 0;
+    // this block has read every length: the last block to say so may overwrite them
+    __threadfence();
+    last = atomicAdd(a.c.state + 1, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  const auto served = [&](int b) { return kv[b] >= 0 && cum_page[b + 1] <= n_free; };
+
+  const int64_t total = min((int64_t)cum_new[a.B], a.capacity);
+  if (threadIdx.x == 0 && (cum_new[a.B] > a.capacity || cum_page[a.B] > n_free)) bad = 1;
+  const int64_t step = (int64_t)gridDim.x * SLOT_THREADS;
+  for (int64_t t = (int64_t)blockIdx.x * SLOT_THREADS + threadIdx.x; t < total; t += step) {
+    const int b = find_last(cum_new, a.B, (int32_t)t);
+    const int32_t have = kv[b] & 0x7fffffff, pos = (int32_t)((uint32_t)have + (uint32_t)(t - cum_new[b]));
+    int64_t slot = -1;
+    if (served(b)) {
+      const int32_t blk = pos >> P, held = (int32_t)(((int64_t)have + (1 << P) - 1) >> P);
+      const int32_t page = blk < held ? a.block_table[b * a.table_stride + blk]
+                                      : a.free_pages[n_free - 1 - (cum_page[b] + blk - held)];
+      if (page >= 0 && page < a.c.n_pages) slot = ((int64_t)page << P) + (pos & ((1 << P) - 1));
+      else bad = 1;
+    }
+    a.slots[t] = slot;
+    a.positions[t] = pos;
+  }
+  const int64_t pages = min((int64_t)cum_page[a.B], n_free);
+  for (int64_t k = (int64_t)blockIdx.x * SLOT_THREADS + threadIdx.x; k < pages; k += step) {
+    const int b = find_last(cum_page, a.B, (int32_t)k);
+    if (!served(b)) continue;
+    const int32_t held = (int32_t)(((int64_t)kv[b] + (1 << P) - 1) >> P);
+    a.block_table[b * a.table_stride + held + (int32_t)(k - cum_page[b])] = a.free_pages[n_free - 1 - k];
+  }
+  if (last) {
+    int64_t taken = 0;
+    for (int b = threadIdx.x; b < a.B; b += SLOT_THREADS) {
+      const int32_t n = cum_new[b + 1] - cum_new[b];
+      // a refused negative length is handed back as it came
+      a.kv_out[b] = kv[b] >= 0 ? kv[b] + (served(b) ? n : 0) : a.kv_lens[b];
+      a.cu_new[b + 1] = cum_new[b + 1];
+      if (cum_page[b + 1] <= n_free) taken = max(taken, (int64_t)cum_page[b + 1]);
+    }
+    // the pages handed out are the largest running sum that fits
+    for (int o = 16; o > 0; o >>= 1) taken = max(taken, __shfl_xor_sync(0xffffffffu, taken, o));
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = taken;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 0; w < SLOT_THREADS / 32; ++w) taken = max(taken, sums[w]);
+      a.cu_new[0] = 0;
+      *a.n_free_out = (int32_t)(n_free - taken);
+      a.c.state[1] = 0;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && bad) atomicOr(a.c.state, DEV_ERR_BOUNDS);
+}
+
+struct ReleaseArgs {
+  Kv4View c;
+  const int32_t* ids;
+  int32_t *kv_lens, *block_table, *free_pages, *n_free;
+  int64_t table_stride;
+  int32_t n, B, max_blocks;
+};
+
+// One block: a running sum of the released requests' pages gives each its place on the stack.
+__global__ void __launch_bounds__(SLOT_THREADS) kv4_release_kernel(const ReleaseArgs a) {
+  extern __shared__ int32_t sm[];
+  int32_t* ids = sm;            // [n]
+  int32_t* cum = ids + a.n;     // [n + 1]
+  __shared__ int64_t sums[32];
+  __shared__ int bad;
+  if (threadIdx.x == 0) bad = 0;
+  for (int i = threadIdx.x; i < a.n; i += SLOT_THREADS) ids[i] = a.ids[i];
+  __syncthreads();
+  int64_t n_free = *a.n_free;
+  if (n_free < 0 || n_free > a.c.n_pages) {
+    if (threadIdx.x == 0) bad = 1;
+    n_free = n_free < 0 ? 0 : a.c.n_pages;
+  }
+  int64_t run = 0;
+  for (int i0 = 0; i0 < a.n; i0 += SLOT_THREADS) {
+    const int i = i0 + threadIdx.x;
+    int64_t pages = 0;
+    if (i < a.n) {
+      const int32_t id = ids[i];
+      bool ok = id >= 0 && id < a.B;
+      if (!ok) bad = 1;
+      for (int j = 0; ok && j < i; ++j) ok = ids[j] != id;  // named before: counted there
+      if (ok) {
+        const int64_t len = a.kv_lens[id];
+        pages = len > 0 ? (len + a.c.page_tokens() - 1) >> a.c.page_shift : 0;
+        if (len < 0 || pages > a.max_blocks) bad = 1;
+        pages = min(pages, (int64_t)a.max_blocks);
+      }
+    }
+    const int64_t c = block_scan(pages, sums) + run;
+    if (i < a.n) cum[i + 1] = (int32_t)min(c, (int64_t)0x7fffffff);
+    if (threadIdx.x == SLOT_THREADS - 1) sums[31] = c;
+    __syncthreads();
+    run = sums[31];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) cum[0] = 0;
+  __syncthreads();
+  const int64_t room = a.c.n_pages - n_free;
+  if (threadIdx.x == 0 && run > room) bad = 1;
+  const int64_t total = min(run, room);
+  for (int64_t k = threadIdx.x; k < total; k += SLOT_THREADS) {
+    const int i = find_last(cum, a.n, (int32_t)k);
+    int32_t* entry = a.block_table + ids[i] * a.table_stride + (k - cum[i]);
+    const int32_t page = *entry;
+    if (page < 0 || page >= a.c.n_pages) bad = 1;
+    a.free_pages[n_free + k] = page;
+    *entry = -1;
+  }
+  for (int i = threadIdx.x; i < a.n; i += SLOT_THREADS)
+    if (ids[i] >= 0 && ids[i] < a.B) a.kv_lens[ids[i]] = 0;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    *a.n_free = (int32_t)(n_free + total);
+    if (bad) atomicOr(a.c.state, DEV_ERR_BOUNDS);
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// write and read
+// ---------------------------------------------------------------------------------------
+constexpr int ROW_THREADS = 128;
+
+struct RowArgs {
+  Kv4View c;
+  __nv_bfloat16 *K, *V;
+  int64_t k_head, k_row, v_head, v_row;
+  const int64_t* slots;
+  int64_t T;
+};
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t bf_pack(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Eight channels of a row (lane l of 16: channels 8 l .. 8 l + 7) to eight codes in channel order,
+// and the group's (step, lo) word.  The product (x - lo) * r is rounded to a whole number in one
+// step, by adding 1.5 * 2^23 in the same fused operation: a value next to a border falls on its own
+// side, as it would in 64 bits.
+template <int NG>
+__device__ __forceinline__ uint32_t quantise8(const uint4& v, uint32_t& scale_word) {
+  float x[8];
+  x[0] = bf_lo(v.x), x[1] = bf_hi(v.x), x[2] = bf_lo(v.y), x[3] = bf_hi(v.y);
+  x[4] = bf_lo(v.z), x[5] = bf_hi(v.z), x[6] = bf_lo(v.w), x[7] = bf_hi(v.w);
+  float lo = x[0], hi = x[0], nan = 0.f;
+#pragma unroll
+  for (int e = 1; e < 8; ++e) lo = fminf(lo, x[e]), hi = fmaxf(hi, x[e]);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) nan += x[e] * 0.f;  // 0, or NaN if any is not finite
+#pragma unroll
+  for (int o = 8 / NG; o > 0; o >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    nan += __shfl_xor_sync(0xffffffffu, nan, o);
+  }
+  const float range = hi - lo;
+  float step = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(range, 15.f)));
+  if (step < 0x1p-126f) step = 0.f;
+  const float r = step > 0.f ? __fdiv_rn(1.f, step) : 0.f;
+  uint32_t code = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float m = fmaf(__fsub_rn(x[e], lo), r, 12582912.f);
+    code |= min(__float_as_uint(m) - 0x4b400000u, 15u) << (4 * e);
+  }
+  scale_word = (__float_as_uint(step) >> 16) | (__float_as_uint(lo) & 0xffff0000u);
+  if (!(nan == 0.f) || !(range < __int_as_float(0x7f800000))) scale_word = 0x7fc07fc0u, code = 0;
+  return code;
+}
+
+// Sixteen lanes take one (token, KV head): 16 bytes of K and of V each.  Bound by HBM: 512 bytes
+// read and 2 (64 + 4 NG) written per row.
+template <int NG>
+__global__ void __launch_bounds__(ROW_THREADS) kv4_append_kernel(const RowArgs a) {
+  using Blk = Kv4Block<NG>;
+  const int l = threadIdx.x & 15;
+  const int64_t item = (int64_t)blockIdx.x * (ROW_THREADS / 16) + (threadIdx.x >> 4);
+  const int64_t t = item / a.c.Hkv;
+  const int h = (int)(item - t * a.c.Hkv);
+  int64_t slot = -1;
+  if (t < a.T) slot = a.slots[t];
+  if (slot >= a.c.n_slots()) {
+    if (l == 0) atomicOr(a.c.state, DEV_ERR_BOUNDS);
+    slot = -1;
+  }
+  uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
+  if (slot >= 0) {
+    kx = *reinterpret_cast<const uint4*>(a.K + h * a.k_head + t * a.k_row + l * 8);
+    vx = *reinterpret_cast<const uint4*>(a.V + h * a.v_head + t * a.v_row + l * 8);
+  }
+  uint32_t ks, vs;
+  const uint32_t kc = quantise8<NG>(kx, ks), vc = quantise8<NG>(vx, vs);
+  // V words hold four channels of two neighbouring quarters of the row (lanes l and l ^ 4): each
+  // lane hands over the half that its partner stores
+  const int q = l >> 2, g = 2 * (l & 3) + (q & 1);
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, vc, 4);
+  const uint32_t vw = (q & 1) ? __byte_perm(other, vc, 0x7632) : __byte_perm(vc, other, 0x5410);
+  if (slot < 0) return;
+  const int i = (int)(slot & 15);
+  uint8_t* blk = a.c.pages + ((slot >> a.c.page_shift) * a.c.Hkv + h) * a.c.page_bytes +
+                 ((slot & (a.c.page_tokens() - 1)) >> 4) * Blk::BYTES;
+  *reinterpret_cast<uint32_t*>(blk + 64 * i + 16 * (l & 3) + 4 * (l >> 2)) = kc;
+  *reinterpret_cast<uint32_t*>(blk + Blk::V_CODES + 64 * i + 8 * (g ^ kv4_v_swizzle(i)) + 4 * (q >> 1)) = vw;
+  if (l % (16 / NG) == 0) {
+    const int grp = l / (16 / NG);
+    *reinterpret_cast<uint32_t*>(blk + Blk::K_SCALES + 4 * NG * i + 4 * grp) = ks;
+    *reinterpret_cast<uint32_t*>(blk + Blk::V_SCALES + 4 * NG * i + 4 * grp) = vs;
+  }
+}
+
+__device__ __forceinline__ uint4 dequantise8(uint32_t code, uint32_t scale_word) {
+  const float step = bf_lo(scale_word), lo = bf_hi(scale_word);
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = fmaf((float)((code >> (4 * e)) & 15u), step, lo);
+  return make_uint4(bf_pack(x[0], x[1]), bf_pack(x[2], x[3]), bf_pack(x[4], x[5]), bf_pack(x[6], x[7]));
+}
+
+template <int NG>
+__global__ void __launch_bounds__(ROW_THREADS) kv4_read_kernel(const RowArgs a) {
+  using Blk = Kv4Block<NG>;
+  const int l = threadIdx.x & 15;
+  const int64_t item = (int64_t)blockIdx.x * (ROW_THREADS / 16) + (threadIdx.x >> 4);
+  const int64_t t = item / a.c.Hkv;
+  const int h = (int)(item - t * a.c.Hkv);
+  int64_t slot = -1;
+  if (t < a.T) slot = a.slots[t];
+  if (slot >= a.c.n_slots()) {
+    if (l == 0) atomicOr(a.c.state, DEV_ERR_BOUNDS);
+    slot = -1;
+  }
+  const int q = l >> 2, g = 2 * (l & 3) + (q & 1);
+  uint32_t kc = 0, vw = 0, ks = 0, vs = 0;
+  if (slot >= 0) {
+    const int i = (int)(slot & 15);
+    const uint8_t* blk = a.c.pages + ((slot >> a.c.page_shift) * a.c.Hkv + h) * a.c.page_bytes +
+                         ((slot & (a.c.page_tokens() - 1)) >> 4) * Blk::BYTES;
+    kc = *reinterpret_cast<const uint32_t*>(blk + 64 * i + 16 * (l & 3) + 4 * (l >> 2));
+    vw = *reinterpret_cast<const uint32_t*>(blk + Blk::V_CODES + 64 * i + 8 * (g ^ kv4_v_swizzle(i)) + 4 * (q >> 1));
+    const int grp = l / (16 / NG);
+    ks = *reinterpret_cast<const uint32_t*>(blk + Blk::K_SCALES + 4 * NG * i + 4 * grp);
+    vs = *reinterpret_cast<const uint32_t*>(blk + Blk::V_SCALES + 4 * NG * i + 4 * grp);
+  }
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, vw, 4);
+  const uint32_t vc = (q & 1) ? __byte_perm(other, vw, 0x7632) : __byte_perm(vw, other, 0x5410);
+  if (slot < 0) return;
+  *reinterpret_cast<uint4*>(a.K + h * a.k_head + t * a.k_row + l * 8) = dequantise8(kc, ks);
+  *reinterpret_cast<uint4*>(a.V + h * a.v_head + t * a.v_row + l * 8) = dequantise8(vc, vs);
+}
+
+msa_status row_args(const msa_kv4_cache* cache, const void* K, const void* V, const msa_strides* s,
+                    const int64_t* slots, int64_t T, RowArgs* a) {
+  const msa_status st = kv4_view(cache, &a->c);
+  if (st != MSA_OK) return st;
+  if (!s || T < 0) return MSA_ERR_INVALID_ARG;
+  if (T == 0) return MSA_OK;
+  if (!K || !V || !slots) return MSA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(K) | reinterpret_cast<uintptr_t>(V)) & 15) return MSA_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(slots) & 7) return MSA_ERR_ALIGN;
+  if (s->k_head % 8 || s->k_row % 8 || s->v_head % 8 || s->v_row % 8) return MSA_ERR_ALIGN;
+  if (T > (int64_t(1) << 31) || T * cache->Hkv > (int64_t(1) << 33)) return MSA_ERR_UNSUPPORTED;
+  a->K = static_cast<__nv_bfloat16*>(const_cast<void*>(K));
+  a->V = static_cast<__nv_bfloat16*>(const_cast<void*>(V));
+  a->k_head = s->k_head, a->k_row = s->k_row, a->v_head = s->v_head, a->v_row = s->v_row;
+  a->slots = slots;
+  a->T = T;
+  return MSA_OK;
+}
+
+unsigned row_blocks(const RowArgs& a) {
+  return (unsigned)((a.T * a.c.Hkv + ROW_THREADS / 16 - 1) / (ROW_THREADS / 16));
+}
+
+}  // namespace
+}  // namespace msa
+
+using namespace msa;
+
+extern "C" {
+
+size_t msa_kv4_page_bytes(int32_t page_tokens, int32_t group) {
+  if (page_tokens < 16 || page_tokens > 256 || (page_tokens & (page_tokens - 1))) return 0;
+  if (group != 32 && group != 64 && group != 128) return 0;
+  return (size_t)page_tokens * (128 + 8 * (128 / group));
+}
+
+msa_status msa_kv4_slots(const msa_kv4_cache* cache, const int32_t* kv_lens, const int32_t* new_lens, int32_t B,
+                         int32_t* block_table, int64_t table_stride, int32_t max_blocks, const int32_t* free_pages,
+                         const int32_t* n_free, int32_t* kv_lens_out, int32_t* n_free_out, int32_t* cu_new,
+                         int64_t* slots, int32_t* positions, int64_t capacity, void* stream) {
+  SlotArgs a{};
+  const msa_status st = kv4_view(cache, &a.c);
+  if (st != MSA_OK) return st;
+  if (B < 0 || capacity < 0 || max_blocks < 0) return MSA_ERR_INVALID_ARG;
+  if (B > KV4_MAX_B) return MSA_ERR_UNSUPPORTED;
+  if (table_stride < max_blocks) return MSA_ERR_SHAPE;
+  if (!n_free || !n_free_out || !cu_new || !free_pages) return MSA_ERR_INVALID_ARG;
+  if (B && (!kv_lens || !new_lens || !kv_lens_out || (max_blocks && !block_table))) return MSA_ERR_INVALID_ARG;
+  if (capacity && (!slots || !positions)) return MSA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(slots) & 7) return MSA_ERR_ALIGN;
+  // positions and page counts are 32-bit: a row holds fewer than 2^31 tokens
+  if (((int64_t)max_blocks << a.c.page_shift) > 0x7fffffff) return MSA_ERR_UNSUPPORTED;
+  a.kv_lens = kv_lens, a.new_lens = new_lens, a.free_pages = free_pages, a.n_free = n_free;
+  a.block_table = block_table, a.kv_out = kv_lens_out, a.n_free_out = n_free_out, a.cu_new = cu_new;
+  a.positions = positions, a.slots = slots, a.table_stride = table_stride, a.capacity = capacity;
+  a.B = B, a.max_blocks = max_blocks;
+  // one block for a decode batch; more only where there are tokens for them
+  const int64_t want = (capacity + 4 * SLOT_THREADS - 1) / (4 * SLOT_THREADS);
+  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(want, 2 * sm_count()));
+  const size_t smem = (3 * (size_t)B + 2) * sizeof(int32_t);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MSA_ERR_CUDA;
+  static std::atomic<uint64_t> ready{0};
+  if (device_pending(ready, dev)) {
+    if (cudaFuncSetAttribute(kv4_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)((3 * KV4_MAX_B + 2) * sizeof(int32_t))) != cudaSuccess)
+      return MSA_ERR_CUDA;
+    mark_device(ready, dev);
+  }
+  count_launches(1);
+  kv4_slots_kernel<<<grid, SLOT_THREADS, smem, static_cast<cudaStream_t>(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+}
+
+msa_status msa_kv4_release(const msa_kv4_cache* cache, const int32_t* ids, int32_t n, int32_t* kv_lens, int32_t B,
+                           int32_t* block_table, int64_t table_stride, int32_t max_blocks, int32_t* free_pages,
+                           int32_t* n_free, void* stream) {
+  ReleaseArgs a{};
+  const msa_status st = kv4_view(cache, &a.c);
+  if (st != MSA_OK) return st;
+  if (n < 0 || B < 0 || max_blocks < 0) return MSA_ERR_INVALID_ARG;
+  if (n > KV4_MAX_B) return MSA_ERR_UNSUPPORTED;
+  if (table_stride < max_blocks) return MSA_ERR_SHAPE;
+  if (n == 0) return MSA_OK;
+  if (!ids || !kv_lens || !block_table || !free_pages || !n_free) return MSA_ERR_INVALID_ARG;
+  a.ids = ids, a.kv_lens = kv_lens, a.block_table = block_table, a.free_pages = free_pages, a.n_free = n_free;
+  a.table_stride = table_stride, a.n = n, a.B = B, a.max_blocks = max_blocks;
+  count_launches(1);
+  kv4_release_kernel<<<1, SLOT_THREADS, (2 * (size_t)n + 1) * sizeof(int32_t), static_cast<cudaStream_t>(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+}
+
+msa_status msa_kv4_append(const msa_kv4_cache* cache, const void* K, const void* V, const msa_strides* strides,
+                          const int64_t* slots, int64_t T, void* stream) {
+  RowArgs a{};
+  const msa_status st = row_args(cache, K, V, strides, slots, T, &a);
+  if (st != MSA_OK || T == 0) return st;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  count_launches(1);
+  switch (cache->group) {
+    case 128: kv4_append_kernel<1><<<row_blocks(a), ROW_THREADS, 0, cs>>>(a); break;
+    case 64: kv4_append_kernel<2><<<row_blocks(a), ROW_THREADS, 0, cs>>>(a); break;
+    default: kv4_append_kernel<4><<<row_blocks(a), ROW_THREADS, 0, cs>>>(a); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+}
+
+msa_status msa_kv4_read(const msa_kv4_cache* cache, void* K, void* V, const msa_strides* strides,
+                        const int64_t* slots, int64_t T, void* stream) {
+  RowArgs a{};
+  const msa_status st = row_args(cache, K, V, strides, slots, T, &a);
+  if (st != MSA_OK || T == 0) return st;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  count_launches(1);
+  switch (cache->group) {
+    case 128: kv4_read_kernel<1><<<row_blocks(a), ROW_THREADS, 0, cs>>>(a); break;
+    case 64: kv4_read_kernel<2><<<row_blocks(a), ROW_THREADS, 0, cs>>>(a); break;
+    default: kv4_read_kernel<4><<<row_blocks(a), ROW_THREADS, 0, cs>>>(a); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+}
+
+msa_status msa_kv4_status(const msa_kv4_cache* cache, void* stream) {
+  Kv4View v;
+  const msa_status st = kv4_view(cache, &v);
+  if (st != MSA_OK) return st;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  uint32_t err = 0;
+  if (cudaMemcpyAsync(&err, v.state, 4, cudaMemcpyDeviceToHost, cs) != cudaSuccess) return MSA_ERR_CUDA;
+  if (cudaStreamSynchronize(cs) != cudaSuccess) return MSA_ERR_CUDA;
+  if (err) {
+    if (cudaMemsetAsync(v.state, 0, 4, cs) != cudaSuccess) return MSA_ERR_CUDA;
+    if (cudaStreamSynchronize(cs) != cudaSuccess) return MSA_ERR_CUDA;
+  }
+  if (err & DEV_ERR_TIMEOUT) return MSA_ERR_TIMEOUT;
+  if (err & DEV_ERR_BOUNDS) return MSA_ERR_DEVICE_BOUNDS;
+  return MSA_OK;
+}
+
+}  // extern "C"

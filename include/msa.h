@@ -334,6 +334,130 @@ msa_status msa_vslash_estimate_static(const void* Q, const void* K, int64_t L, i
                                       int64_t k_row_stride, float scale, int32_t k_v, int32_t k_s, int32_t* v_out,
                                       int32_t* s_out, int32_t* counts_out, void* stream);
 
+/* ---- what makes the queries and keys: per-head norm and rotary position embedding ----
+ *
+ * One pass over Q [Hq][T][128] and K [Hkv][T][128] (bf16): every row x is normalised,
+ * x * rsqrt(mean(x^2) + eps) * w (RMS norm over the head's 128 channels; wq / wk bf16 [128],
+ * 16-byte aligned; NULL: rows are taken as they are), then its first `dim` channels are rotated:
+ * pair (a, b) of frequency i becomes (a cos f - b sin f, b cos f + a sin f) * scale,
+ * f = position * inv_freq[i], pairs (i, i + dim / 2) (RoFormer; half-split, as the workload
+ * generator's rotary inputs) or, interleaved, (2 i, 2 i + 1).  Channels from `dim` on are passed
+ * on unrotated and unscaled.  fp32 arithmetic, one rounding to bf16; the angle is exact modulo
+ * one turn for every int32 position (negative ones too).
+ *  - positions: device int32 [n_axes][pos_stride >= T]; frequency i uses axis a of the sections[a]
+ *    frequencies it falls in (time / height / width positions of video tokens; one axis: sections
+ *    is ignored).
+ *  - in / out strides: element strides, as for Q and K of the layer calls (q_head, q_row, k_head,
+ *    k_row).  Qo / Ko may be Q / K themselves (same pointer and strides); any other overlap is not
+ *    supported.  Hq or Hkv may be 0 (its pointers are then ignored).  T = 0 does nothing.
+ * Asynchronous on `stream`; allocates nothing. */
+typedef struct {
+  int32_t dim;          /* rotated channels: a multiple of 16, 0 (norm alone) .. 128 */
+  int32_t interleaved;  /* 0: pairs (i, i + dim / 2); 1: pairs (2 i, 2 i + 1) */
+  int32_t n_axes;       /* position axes, 1 .. 4 */
+  int32_t sections[4];  /* frequencies per axis, summing to dim / 2 (n_axes > 1) */
+  float scale;          /* factor of the rotated channels (1 where a model has none) */
+  double inv_freq[64];  /* radians per position, dim / 2 of them */
+} msa_rope;
+
+msa_status msa_qk_norm_rope(const void* Q, const void* K, const msa_strides* in, void* Qo, void* Ko,
+                            const msa_strides* out, int64_t T, int32_t Hq, int32_t Hkv, const void* wq, const void* wk,
+                            float eps, const msa_rope* rope, const int32_t* positions, int64_t pos_stride,
+                            void* stream);
+
+/* ---- what holds the keys and values afterwards: a paged 4-bit cache ----
+ *
+ * One layer's cache: pages [n_pages][Hkv][page_bytes], each of `page_tokens` tokens, in blocks of
+ * 16 tokens.  A row of 128 channels is held as 4-bit codes in groups of `group` channels with the
+ * group's step and minimum in bf16: with lo, hi the group's smallest and largest value,
+ *   step = bf16((hi - lo) / 15)  (0 below the smallest normal number),
+ *   code = round-to-even((x - lo) * fp32(1 / step)),   value = lo + code * step.
+ * A group that holds a NaN or an infinity, or whose hi - lo overflows fp32, is held as NaN.
+ * A block's bytes, NG = 128 / group, token i in [0, 16):
+ *   64 i:                     K codes, channel x in byte 16 (x % 32 / 8) + 4 (x / 32) + x % 8 / 2
+ *   1024 + 64 i:              V codes, channel x in byte
+ *                             8 ((x % 32 / 4) ^ (4 (i / 2 % 2))) + 2 (x / 32) + x % 4 / 2
+ *   2048 + 4 NG i:            K (step, lo) per group;   2048 + 64 NG + 4 NG i: V (step, lo)
+ * (even channels in the low nibble): the order in which the attention kernel's lanes read whole
+ * words.  A token's slot is page * page_tokens + offset.
+ *
+ * `state`: 64 bytes of device memory, zero-filled once by the caller: the cache's error word (read
+ * and cleared by msa_kv4_status) and a launch-internal counter.  msa_kv4_read and msa_kv4_attend
+ * only read the pages and may overlap on the GPU with one another; every other call on a cache is
+ * ordered against all calls on it. */
+typedef struct {
+  void* pages;          /* device, 16-byte aligned */
+  int64_t n_pages;      /* 1 .. 2^31 - 1 */
+  int32_t page_tokens;  /* 16, 32, 64, 128 or 256 */
+  int32_t Hkv;          /* 1 .. 1024 */
+  int32_t group;        /* 32, 64 or 128 */
+  int32_t _pad;
+  void* state;          /* device, 64 bytes, 16-byte aligned */
+} msa_kv4_cache;
+
+/* Bytes of one page of one KV head: page_tokens * (128 + 8 * 128 / group); 0 for sizes the cache
+ * does not have. */
+size_t msa_kv4_page_bytes(int32_t page_tokens, int32_t group);
+
+/* Block tables and slot maps from request lengths.  Request b holds kv_lens[b] tokens in
+ * ceil(kv_lens[b] / page_tokens) pages, the leading entries of its row of block_table
+ * [B][table_stride >= max_blocks] (int32), and is given new_lens[b] more: pages are taken from the
+ * top of the stack free_pages[0 .. *n_free) (int32, room for n_pages entries), in the order of the requests,
+ * and written to its row.  Outputs: kv_lens_out[b] = kv_lens[b] + new_lens[b], *n_free_out (each may
+ * be its input), cu_new[B + 1] (running sum of new_lens), and for token t of cu_new[b] + i: slots[t]
+ * (int64) and positions[t] = kv_lens[b] + i, for t below `capacity`; entries behind the last token
+ * are left as they were.
+ * A request that does not fit its row (or has a negative length, whose new tokens then count as
+ * none) gets no pages; from the first request on that the free pages do not suffice for, none
+ * does: their slots are -1, kv_lens_out = kv_lens, and the error is recorded (msa_kv4_status).
+ * B <= 4096.  Every pointer is a device pointer. */
+msa_status msa_kv4_slots(const msa_kv4_cache* cache, const int32_t* kv_lens, const int32_t* new_lens, int32_t B,
+                         int32_t* block_table, int64_t table_stride, int32_t max_blocks, const int32_t* free_pages,
+                         const int32_t* n_free, int32_t* kv_lens_out, int32_t* n_free_out, int32_t* cu_new,
+                         int64_t* slots, int32_t* positions, int64_t capacity, void* stream);
+
+/* Gives back the pages of the requests ids[0 .. n): pushed on the free stack in the order of the
+ * list, their kv_lens set to 0 and their table entries to -1.  An id named twice counts once; an id
+ * outside [0, B) is recorded as an error.  n <= 4096. */
+msa_status msa_kv4_release(const msa_kv4_cache* cache, const int32_t* ids, int32_t n, int32_t* kv_lens, int32_t B,
+                           int32_t* block_table, int64_t table_stride, int32_t max_blocks, int32_t* free_pages,
+                           int32_t* n_free, void* stream);
+
+/* Quantises K and V [Hkv][T][128] (bf16, strides k_* and v_*) into the cache at slots[0 .. T)
+ * (device int64).  A negative slot skips its token; a slot behind the last page is recorded as an
+ * error and skipped.  Slots are distinct: of a slot named twice the row is undefined (its
+ * neighbours are not affected). */
+msa_status msa_kv4_append(const msa_kv4_cache* cache, const void* K, const void* V, const msa_strides* strides,
+                          const int64_t* slots, int64_t T, void* stream);
+
+/* The values of the tokens at slots[0 .. T), rounded once to bf16, into K and V [Hkv][T][128]
+ * (strides k_* and v_*): a cached prefix as the layer calls read it.  Rows of negative slots, and
+ * of slots behind the last page (recorded as an error), are left as they were. */
+msa_status msa_kv4_read(const msa_kv4_cache* cache, void* K, void* V, const msa_strides* strides,
+                        const int64_t* slots, int64_t T, void* stream);
+
+/* Attention over the cache: request b's query tokens are rows cu_q[b] .. cu_q[b + 1) of Q
+ * [Hq][total_q][128] and the last of its kv_lens[b] cached tokens (append them first), so query i of
+ * n sees the keys j <= kv_lens[b] - n + i:  O = softmax(Q K^T * scale) V over the values the cache
+ * stands for (bf16), lse (optional, fp32 [Hq][total_q]) the natural-log normaliser.  A row that sees
+ * no key has O = 0 and lse = -inf.  Rows behind cu_q[B] are left as they were.  Query head h reads KV
+ * head h / (Hq / Hkv).  Any number of query tokens per request (one each: decoding; a few: draft
+ * verification; many: a prompt over a cached prefix); max_q, the most of any request, picks the
+ * kernel's tile and nothing else.  Page numbers outside the cache hide their keys, lengths outside
+ * the table row or Q are cut, and both are recorded as an error.  B <= 4096.
+ * ws: device, 256-byte aligned, msa_kv4_attend_workspace_bytes() bytes, zero-filled once by the
+ * caller; every call leaves it ready for the next, of any shape.  Calls that may overlap on the GPU
+ * need a workspace each.  Sums in fp32 and in a fixed order: the same inputs give the same bits. */
+size_t msa_kv4_attend_workspace_bytes(void);
+msa_status msa_kv4_attend(const msa_kv4_cache* cache, const void* Q, void* O, const msa_strides* strides,
+                          int32_t total_q, int32_t Hq, float scale, const int32_t* block_table, int64_t table_stride,
+                          int32_t max_blocks, const int32_t* kv_lens, const int32_t* cu_q, int32_t B, int32_t max_q,
+                          float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Synchronises `stream`, returns the first error the calls on this cache recorded on the device
+ * (MSA_ERR_DEVICE_BOUNDS, MSA_ERR_TIMEOUT, or MSA_OK) and clears it. */
+msa_status msa_kv4_status(const msa_kv4_cache* cache, void* stream);
+
 /* Number of CUDA kernels this library has launched since it was loaded (all plans, all
  * threads); lets a caller count the kernels of one call by differencing. */
 uint64_t msa_kernel_launches(void);
