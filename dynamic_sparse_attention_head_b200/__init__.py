@@ -462,239 +462,19 @@ def weight_share(Q, K, scale: float, heads, rows, recall: float = 0.95, stream=N
     return out
 
 
-# ---- queries and keys before the layer; keys and values after it --------------------------
-def _tensor(name, t, dtype, dim, device, contiguous=True):
-    """Checks one argument tensor: type, dimensions, device and layout."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: a tensor is wanted")
-    if t.dtype != dtype or t.dim() != dim:
-        raise ValueError(f"{name}: a {dim}-dimensional tensor of {dtype} is wanted, got {tuple(t.shape)} {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the others on {device}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} has to be contiguous")
-    return t
-
-
-def _rows(name, t, heads, tokens, device):
-    """Checks a [heads, tokens, 128] bf16 tensor whose rows are contiguous."""
-    import torch
-    _tensor(name, t, torch.bfloat16, 3, device, contiguous=False)
-    if t.shape[2] != 128 or (t.stride(2) != 1 and t.numel()) or (heads is not None and t.shape[0] != heads) or \
-            (tokens is not None and t.shape[1] != tokens):
-        raise ValueError(f"{name}: [{'H' if heads is None else heads}, {'T' if tokens is None else tokens}, 128] with "
-                         f"contiguous rows is wanted, got {tuple(t.shape)} with strides {t.stride()}")
-    return t
-
-
-def _on(device, stream):
-    """Device guard of a call on `device`, and its stream there."""
-    import torch
-    if device.type != "cuda":
-        raise ValueError(f"CUDA tensors are wanted, got {device}")
-    return torch.cuda.device(device), (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
-
-
-class Rope:
-    """Rotary position embedding of msa_qk_norm_rope: `dim` rotated channels (a multiple of 16), the
-    frequencies from `base` (inv_freq[i] = base ** (-2 i / dim)) or given (dim / 2 of them: scaled
-    variants), pairs (i, i + dim / 2) or, interleaved, (2 i, 2 i + 1).  `sections`: frequencies of each
-    position axis (video tokens: time, height, width), summing to dim / 2; None: one axis.  `scale`
-    multiplies the rotated channels."""
-
-    def __init__(self, dim: int = 128, base: float = 1e6, inv_freq: Optional[Sequence[float]] = None,
-                 interleaved: bool = False, sections: Optional[Sequence[int]] = None, scale: float = 1.0):
-        if dim < 0 or dim > 128 or dim % 16:
-            raise ValueError("dim: a multiple of 16 up to 128 is wanted")
-        freq = [float(base) ** (-2.0 * i / dim) for i in range(dim // 2)] if inv_freq is None else \
-            [float(f) for f in inv_freq]
-        if len(freq) != dim // 2:
-            raise ValueError(f"inv_freq: {dim // 2} frequencies are wanted, got {len(freq)}")
-        sec = [dim // 2] if sections is None else [int(x) for x in sections]
-        if not 1 <= len(sec) <= 4 or min(sec) < 0 or sum(sec) != dim // 2:
-            raise ValueError(f"sections: up to 4 counts that sum to {dim // 2} are wanted, got {sec}")
-        self.n_axes = len(sec)
-        self._c = RopeC(dim=dim, interleaved=int(bool(interleaved)), n_axes=len(sec), scale=float(scale))
-        for i, f in enumerate(freq):
-            self._c.inv_freq[i] = f
-        for i, x in enumerate(sec):
-            self._c.sections[i] = x
-
-
-def qk_norm_rope(Q, K, Qo, Ko, positions, rope: Rope, wq=None, wk=None, eps: float = 1e-6, stream=None):
-    """msa_qk_norm_rope: RMS norm of every head's rows (weights wq / wk bf16 [128]; None: no norm) and
-    the rotation at `positions`, in one pass.  Q, Qo [Hq, T, 128], K, Ko [Hkv, T, 128]: bf16 CUDA
-    tensors, any head and token strides that are multiples of 8 (the projection's [T, H, 128]
-    transposed); Qo / Ko may be Q / K.  positions: int32 [T], or [axes, T] for a rope with sections."""
-    import torch
-    dev = _rows("Q", Q, None, None, None).device
-    T = Q.shape[1]
-    _rows("K", K, None, T, dev)
-    _rows("Qo", Qo, Q.shape[0], T, dev)
-    _rows("Ko", Ko, K.shape[0], T, dev)
-    pos = _tensor("positions", positions, torch.int32, positions.dim(), dev, contiguous=False)
-    if pos.dim() == 1:
-        pos = pos.unsqueeze(0)
-    if pos.dim() != 2 or tuple(pos.shape) != (rope.n_axes, T) or (T > 1 and pos.stride(1) != 1):
-        raise ValueError(f"positions: int32 [{rope.n_axes}, {T}] with contiguous rows is wanted, got "
-                         f"{tuple(positions.shape)}")
-    for name, w in (("wq", wq), ("wk", wk)):
-        if w is not None and _tensor(name, w, torch.bfloat16, 1, dev).numel() != 128:
-            raise ValueError(f"{name}: 128 weights are wanted")
-    guard, st = _on(dev, stream)
-    with guard:
-        _check("msa_qk_norm_rope",
-               _lib.msa_qk_norm_rope(Q.data_ptr(), K.data_ptr(), ctypes.byref(_strides(Q=Q, K=K)), Qo.data_ptr(),
-                                     Ko.data_ptr(), ctypes.byref(_strides(Q=Qo, K=Ko)), T, Q.shape[0], K.shape[0],
-                                     wq.data_ptr() if wq is not None else None,
-                                     wk.data_ptr() if wk is not None else None, float(eps), ctypes.byref(rope._c),
-                                     pos.data_ptr(), pos.stride(0), st))
-
-
-def kv4_page_bytes(page: int, group: int) -> int:
-    """Bytes of one page of one KV head: page * (128 + 8 * 128 / group)."""
-    n = int(_lib.msa_kv4_page_bytes(int(page), int(group)))
-    if not n:
-        raise ValueError(f"page: 16, 32, 64, 128 or 256 tokens, group: 32, 64 or 128 channels; got {page}, {group}")
-    return n
-
-
-class KV4Cache:
-    """One layer's paged 4-bit K/V cache (msa_kv4_cache): `pages` uint8 [n_pages, Hkv, kv4_page_bytes(page,
-    group)] on the GPU, `page` tokens a page, `group` channels a scale.  `KV4Cache.alloc` makes the
-    pages too.  Calls on one cache run in stream order; a CUDA graph may hold any of them."""
-
-    def __init__(self, pages, page: int = 64, group: int = 64):
-        import torch
-        want = kv4_page_bytes(page, group)
-        _tensor("pages", pages, torch.uint8, 3, None)
-        if pages.shape[2] != want:
-            raise ValueError(f"pages: [n_pages, Hkv, {want}] is wanted, got {tuple(pages.shape)}")
-        if pages.device.type != "cuda":
-            raise ValueError(f"pages: a CUDA tensor is wanted, got {pages.device}")
-        self.pages, self.page, self.group = pages, int(page), int(group)
-        self.n_pages, self.Hkv = int(pages.shape[0]), int(pages.shape[1])
-        self.device = pages.device
-        self.state = torch.zeros(64, dtype=torch.uint8, device=pages.device)
-        self._c = KV4CacheC(pages=pages.data_ptr(), n_pages=self.n_pages, page_tokens=self.page, Hkv=self.Hkv,
-                            group=self.group, state=self.state.data_ptr())
-
-    @classmethod
-    def alloc(cls, n_pages: int, Hkv: int, page: int = 64, group: int = 64, device="cuda") -> "KV4Cache":
-        import torch
-        return cls(torch.zeros(n_pages, Hkv, kv4_page_bytes(page, group), dtype=torch.uint8, device=device), page, group)
-
-    def alloc_workspace(self, Hq: int = 0):
-        """Zero-filled workspace of `attend` (its size does not depend on the shapes)."""
-        import torch
-        return torch.zeros(int(_lib.msa_kv4_attend_workspace_bytes()), dtype=torch.uint8, device=self.device)
-
-    def _ints(self, name, t, n=None):
-        import torch
-        _tensor(name, t, torch.int32, 1, self.device)
-        if n is not None and t.numel() != n:
-            raise ValueError(f"{name}: {n} entries are wanted, got {t.numel()}")
-        return t
-
-    def _table(self, t, B):
-        import torch
-        _tensor("block_table", t, torch.int32, 2, self.device, contiguous=False)
-        if t.shape[0] != B or (t.shape[1] > 1 and t.stride(1) != 1) or (B > 1 and t.stride(0) < t.shape[1]):
-            raise ValueError(f"block_table: [{B}, blocks] with contiguous rows is wanted, got {tuple(t.shape)}")
-        return t, max(int(t.stride(0)), int(t.shape[1]))
-
-    def slots(self, kv_lens, new_lens, block_table, free_pages, n_free, slots, positions, cu_new, kv_lens_out=None,
-              n_free_out=None, stream=None):
-        """msa_kv4_slots: pages for new_lens[b] more tokens per request, from the top of the free stack
-        free_pages[: n_free]; fills block_table's new entries, cu_new [B + 1], slots (int64) and
-        positions (int32) of the new tokens (entries behind the last are left), and kv_lens / n_free
-        (in place, or in the *_out tensors)."""
-        import torch
-        B = self._ints("kv_lens", kv_lens).numel()
-        self._ints("new_lens", new_lens, B)
-        tab, stride = self._table(block_table, B)
-        self._ints("free_pages", free_pages, self.n_pages)
-        self._ints("n_free", n_free, 1)
-        self._ints("cu_new", cu_new, B + 1)
-        kv_out = self._ints("kv_lens_out", kv_lens if kv_lens_out is None else kv_lens_out, B)
-        nf_out = self._ints("n_free_out", n_free if n_free_out is None else n_free_out, 1)
-        cap = _tensor("slots", slots, torch.int64, 1, self.device).numel()
-        self._ints("positions", positions, cap)
-        guard, st = _on(self.device, stream)
-        with guard:
-            _check("msa_kv4_slots",
-                   _lib.msa_kv4_slots(ctypes.byref(self._c), kv_lens.data_ptr(), new_lens.data_ptr(), B, tab.data_ptr(),
-                                      stride, tab.shape[1], free_pages.data_ptr(), n_free.data_ptr(), kv_out.data_ptr(),
-                                      nf_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr(), positions.data_ptr(), cap,
-                                      st))
-
-    def release(self, ids, kv_lens, block_table, free_pages, n_free, stream=None):
-        """msa_kv4_release: the pages of requests `ids` (int32) go back on the free stack."""
-        n = self._ints("ids", ids).numel()
-        B = self._ints("kv_lens", kv_lens).numel()
-        tab, stride = self._table(block_table, B)
-        self._ints("free_pages", free_pages, self.n_pages)
-        self._ints("n_free", n_free, 1)
-        guard, st = _on(self.device, stream)
-        with guard:
-            _check("msa_kv4_release",
-                   _lib.msa_kv4_release(ctypes.byref(self._c), ids.data_ptr(), n, kv_lens.data_ptr(), B, tab.data_ptr(),
-                                        stride, tab.shape[1], free_pages.data_ptr(), n_free.data_ptr(), st))
-
-    def _kv(self, K, V, slots):
-        import torch
-        T = _tensor("slots", slots, torch.int64, 1, self.device).numel()
-        _rows("K", K, self.Hkv, T, self.device)
-        _rows("V", V, self.Hkv, T, self.device)
-        return T, ctypes.byref(_strides(K=K, V=V))
-
-    def append(self, K, V, slots, stream=None):
-        """msa_kv4_append: quantises K, V [Hkv, T, 128] (bf16) into the cache at `slots` (int64 [T];
-        negative: skipped; each at most once)."""
-        T, s = self._kv(K, V, slots)
-        guard, st = _on(self.device, stream)
-        with guard:
-            _check("msa_kv4_append", _lib.msa_kv4_append(ctypes.byref(self._c), K.data_ptr(), V.data_ptr(), s,
-                                                         slots.data_ptr(), T, st))
-
-    def read(self, slots, K, V, stream=None):
-        """msa_kv4_read: the values at `slots` into K, V [Hkv, T, 128] (bf16)."""
-        T, s = self._kv(K, V, slots)
-        guard, st = _on(self.device, stream)
-        with guard:
-            _check("msa_kv4_read", _lib.msa_kv4_read(ctypes.byref(self._c), K.data_ptr(), V.data_ptr(), s,
-                                                     slots.data_ptr(), T, st))
-
-    def attend(self, Q, O, block_table, kv_lens, cu_q, max_q: int, scale: float, ws, lse=None, stream=None):
-        """msa_kv4_attend: Q, O [Hq, T, 128] (bf16); request b's query tokens are columns cu_q[b] ..
-        cu_q[b + 1) and the last of its kv_lens[b] cached tokens.  max_q: the most query tokens of any
-        request (picks the kernel's tile).  lse: fp32 [Hq, T] or None.  ws: alloc_workspace()."""
-        import torch
-        _rows("Q", Q, None, None, self.device)
-        Hq, T = int(Q.shape[0]), int(Q.shape[1])
-        _rows("O", O, Hq, T, self.device)
-        B = self._ints("kv_lens", kv_lens).numel()
-        self._ints("cu_q", cu_q, B + 1)
-        tab, stride = self._table(block_table, B)
-        if lse is not None and tuple(_tensor("lse", lse, torch.float32, 2, self.device).shape) != (Hq, T):
-            raise ValueError(f"lse: [{Hq}, {T}] is wanted, got {tuple(lse.shape)}")
-        _tensor("ws", ws, torch.uint8, 1, self.device)
-        guard, st = _on(self.device, stream)
-        with guard:
-            _check("msa_kv4_attend",
-                   _lib.msa_kv4_attend(ctypes.byref(self._c), Q.data_ptr(), O.data_ptr(), ctypes.byref(_strides(Q=Q, O=O)),
-                                       T, Hq, float(scale), tab.data_ptr(), stride, tab.shape[1], kv_lens.data_ptr(),
-                                       cu_q.data_ptr(), B, int(max_q), lse.data_ptr() if lse is not None else None,
-                                       ws.data_ptr(), ws.numel(), st))
-
-    def device_status(self, stream=None) -> int:
-        """msa_kv4_status (synchronises): 0, or the first error recorded on the device, which it clears."""
-        guard, st = _on(self.device, stream)
-        with guard:
-            return int(_lib.msa_kv4_status(ctypes.byref(self._c), st))
-
-
 def executed_flops(tiles: int) -> int:
     """FLOPs of the executed 128x128 tiles (QK^T and PV, d = 128)."""
     return 4 * 128 * 128 * 128 * int(tiles)
+
+
+# What stands around the layer (serving.py) needs torch at import; the library itself does not.
+_SERVING = ("Rope", "qk_norm_rope", "KV4Cache", "kv4_page_bytes")
+
+
+def __getattr__(name):
+    if name in _SERVING:
+        from . import serving
+        for n in _SERVING:
+            globals()[n] = getattr(serving, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -3,22 +3,27 @@
 // With k_j = lo_j + step_j c_j per group of channels, the scores need no dequantised key:
 //   s_j = sum_g step_jg (q_g . c_jg) + lo_jg sum(q_g),
 // and with p_j the probabilities, o_g = sum_j (p_j step_jg) c_jg + sum_j p_j lo_jg.  The two
-// contractions run on the bare codes, exact in fp16: a nibble masked out of a packed word IS a pair of
-// fp16 subnormals (value code * 2^-24, or code * 2^-20 for the upper nibble of a byte), so a
-// 32-bit word of eight codes becomes four operand registers with one shift and four ANDs, no
-// conversion and no subtraction.  The factors 2^24 and 16 are taken out where the scales enter.
+// contractions run on the bare codes, exact in fp16.  For the scores a nibble masked out of a packed
+// word IS a pair of fp16 subnormals (value code * 2^-24, or code * 2^-20 for the upper nibble of a
+// byte), so a 32-bit word of eight codes becomes four operand registers with one shift and four
+// ANDs, no conversion and no subtraction.  The factors 2^24 and 16 are taken out where the scales
+// enter.  The values' codes are centred first (code - 8, one more subtraction a pair, and
+// lo + 8 step in place of lo): a tensor core cuts its fp32 sums off instead of rounding them, and
+// a long sum of codes of one sign drifts by that, against the sum of lo that it all but cancels
+// (1M keys: relative error 3.2e-3 with bare codes).
 //
-// One CTA per SM.  The keys of every (request, KV head, tile of query rows) are cut into tiles of 32;
-// the tiles of all of them form one line, of which every CTA takes an equal stretch, whatever the
-// lengths are.  A warp owns every W-th tile of the CTA's stretch: it fetches a tile (two blocks of
-// 16 tokens, K and V codes and scales contiguous) with one or two bulk copies into a ring of its
-// own, so no barrier spans warps while keys stream.  Products are S^T = C_K Q^T and
-// O^T = C_V^T P^T (mma.sync m16n8k16: the codes are the 16-row operand, 8 query rows per column
-// block), each warp with its own running maximum and sums; the warps' results join in shared memory
-// at the end of a segment, and the CTAs' through the workspace, in a fixed order, by the CTA that
-// arrives last.  mma.sync rather than tcgen05: the operands go from shared memory to registers as
-// 4-bit words and are never written back, and at 8 rows a key the products need under half of
-// mma.sync's rate at full HBM bandwidth.
+// One CTA per SM.  The keys of every (request, KV head, tile of query rows) are cut into tiles, with
+// one unit more per such segment for what its start and end cost; the units of all segments form one
+// line, of which every warp takes an equal stretch, whatever the lengths are.  A warp fetches its
+// tiles (blocks of 16 tokens, K and V codes and scales contiguous) with bulk copies into a ring of
+// its own, ahead across segment borders, so no barrier spans warps while keys stream.  Products are
+// S^T = C_K Q^T and O^T = C_V^T P^T (mma.sync m16n8k16: the codes are the 16-row operand, 8 query
+// rows per column block), each warp with its own running maximum and sums.  A segment inside one
+// warp's stretch is written by it; what crosses warps joins in shared memory at the end, what
+// crosses CTAs through the workspace, in a fixed order, by the CTA that arrives last.  mma.sync
+// rather than tcgen05: the operands go from shared memory to registers as 4-bit words and are never
+// written back, and at 8 rows a key the products need about half of mma.sync's rate at full HBM
+// bandwidth.
 //
 // Bound by HBM for long contexts: 2 (64 + 4 NG) bytes per key and KV head.
 #include <cuda_bf16.h>
@@ -26,6 +31,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kernels.h"
 #include "kv4.cuh"
@@ -36,7 +42,6 @@ namespace msa {
 namespace {
 
 constexpr int HD = 128;       // channels
-constexpr int TK = 32;        // keys of a tile
 constexpr int MAX_CTAS = 160;
 constexpr int MAX_ROWS = 16;  // query rows of a tile, most
 constexpr int PART = HD + 2;  // floats of a partial row: O, running maximum, sum
@@ -89,6 +94,19 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Codes in bits 0-3 (4-7) of both halves as fp16 code - 8 (16 (code - 8)): the code is set into the
+// mantissa of 1024, whose step is one, and 1024 + 8 (1024 + 128) is taken off; both are exact.
+__device__ __forceinline__ uint32_t centred_lo(uint32_t w) {
+  const uint32_t v = (w & 0x000f000fu) | 0x64006400u;
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), __half2{__ushort_as_half(0x6408), __ushort_as_half(0x6408)});
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+__device__ __forceinline__ uint32_t centred_hi(uint32_t w) {
+  const uint32_t v = (w & 0x00f000f0u) | 0x64006400u;
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), __half2{__ushort_as_half(0x6480), __ushort_as_half(0x6480)});
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
 // 1 / v of a power of two
 __device__ __forceinline__ float inv_pow2(float v) { return __uint_as_float(0x7f000000u - __float_as_uint(v)); }
 
@@ -121,31 +139,37 @@ __device__ __forceinline__ bool request_lens(const AttendArgs& a, int b, int32_t
   return ok;
 }
 
-template <int NG, int NT, int W, int STAGES>
+template <int NG, int NT, int TK, int W, int STAGES>
 struct AttendSmem {
-  static constexpr int TILE = 2 * Kv4Block<NG>::BYTES;
+  static constexpr int TILE = TK / 16 * Kv4Block<NG>::BYTES;
   static constexpr int ROWS = 8 * NT;
-  static constexpr int JOIN = W / 2;  // warps' results side by side
-  static constexpr int RING = 0;
-  static constexpr int JOIN_AT = W * STAGES * TILE;
-  static constexpr int STAT_AT = JOIN_AT + JOIN * ROWS * HD * 4;  // [JOIN][ROWS][2]
-  static constexpr int BARS = STAT_AT + JOIN * ROWS * 2 * 4;
-  static constexpr int CUM = BARS + W * STAGES * 8 + 64;  // [B + 1]
+  static constexpr int ROW_BYTES = ROWS * HD * 4;
+  static constexpr int RING = 0;  // a warp's tail result lies in its ring once its tiles are used up
+  static constexpr int HEADS = W * STAGES * TILE;                // [W][ROWS][HD]
+  static constexpr int STATS = HEADS + W * ROW_BYTES;            // [W][head, tail][ROWS][2]
+  static constexpr int SEGS = STATS + W * 2 * ROWS * 2 * 4;      // [W + 1]: tails; the CTA's head
+  static constexpr int BARS = SEGS + (W + 1) * (int)sizeof(Segment);
+  static constexpr int CUM = BARS + W * STAGES * 8;              // [B + 1]
+  static_assert(STAGES * TILE >= ROW_BYTES, "a tail result fits the ring");
+  static_assert(BARS % 8 == 0 && CUM % 4 == 0, "alignment");
 };
 
-template <int NG, int NT, int W, int STAGES>
+template <int NG, int NT, int TK, int W, int STAGES>
 __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs a) {
-  using S = AttendSmem<NG, NT, W, STAGES>;
+  using S = AttendSmem<NG, NT, TK, W, STAGES>;
   using Blk = Kv4Block<NG>;
   constexpr int ROWS = 8 * NT;
+  constexpr int MT = TK / 16;  // operand tiles of 16 keys
   constexpr int THREADS = W * 32;
   extern __shared__ __align__(128) uint8_t smem[];
-  float* join = reinterpret_cast<float*>(smem + S::JOIN_AT);
-  float* stat = reinterpret_cast<float*>(smem + S::STAT_AT);
+  float* heads = reinterpret_cast<float*>(smem + S::HEADS);
+  float* stats = reinterpret_cast<float*>(smem + S::STATS);
+  Segment* segs = reinterpret_cast<Segment*>(smem + S::SEGS);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BARS);
   int32_t* cum = reinterpret_cast<int32_t*>(smem + S::CUM);
-  __shared__ int64_t sums[32];
-  __shared__ int abort_flag, bad, arrived_last;
+  __shared__ int64_t sums[W];
+  __shared__ int abort_flag, bad, last_of[2];
+  __shared__ uint8_t ends[W];  // 1: has a head, 2: the head's segment ends in the stretch, 4: has a tail
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
@@ -158,7 +182,8 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
   }
   __syncthreads();
 
-  // ---- the line of tiles: running sum of the requests' tile counts ----
+  // ---- the line of units: running sum of the requests' counts ----
+  const auto units_of = [](int kv) { return 1 + (kv + TK - 1) / TK; };
   int64_t run = 0;
   for (int b0 = 0; b0 < a.B; b0 += THREADS) {
     const int b = b0 + tid;
@@ -166,7 +191,7 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
     if (b < a.B) {
       int32_t q0, n, kv;
       if (!request_lens(a, b, q0, n, kv)) bad = 1;
-      x = (int64_t)row_tiles<NT>(n, a.group) * a.c.Hkv * max(1, (kv + TK - 1) / TK);
+      x = (int64_t)row_tiles<NT>(n, a.group) * a.c.Hkv * units_of(kv);
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -181,19 +206,17 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
     for (int w = 0; w < W; ++w) run += sums[w];
     __syncthreads();
   }
-  if (run > 0x7fffffff) {  // more tiles than the line has numbers for
-    if (tid == 0) atomicOr(a.c.state, DEV_ERR_BOUNDS);
-    return;
-  }
-  if (blockIdx.x == 0 && tid == 0 && bad) atomicOr(a.c.state, DEV_ERR_BOUNDS);
-  // a CTA takes at least a tile per warp where there are that many
+  if (blockIdx.x == 0 && tid == 0 && (bad || run > 0x7fffffff)) atomicOr(a.c.state, DEV_ERR_BOUNDS);
+  if (run > 0x7fffffff) return;  // more units than the line has numbers for
   const int total = (int)run;
+  // a CTA takes at least a unit per warp where there are that many
   const int active = min((int)gridDim.x, max(1, (total + W - 1) / W));
   if ((int)blockIdx.x >= active || total == 0) return;
   const auto edge = [&](int i) { return (int)((int64_t)total * i / active); };
   const int t0 = edge(blockIdx.x), t1 = edge(blockIdx.x + 1);
+  const int w0 = t0 + (int)((int64_t)(t1 - t0) * warp / W), w1 = t0 + (int)((int64_t)(t1 - t0) * (warp + 1) / W);
 
-  const auto locate = [&](int t) {  // the segment that holds tile t
+  const auto locate = [&](int t) {  // the segment that holds unit t
     Segment s;
     int lo = 0, hi = a.B;
     while (hi - lo > 1) {
@@ -203,7 +226,7 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
     }
     s.b = lo;
     request_lens(a, lo, s.q0, s.n, s.kv);
-    s.count = max(1, (s.kv + TK - 1) / TK);
+    s.count = units_of(s.kv);
     const int i = (t - cum[lo]) / s.count;
     const int rts = row_tiles<NT>(s.n, a.group);
     s.h = i / rts;
@@ -217,75 +240,81 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
     return s.kv - s.n + last_row / a.group + 1;
   };
 
-  // ---- this warp's ring: tiles t0 + warp, + W, ... in order, across segments ----
+  // ---- this warp's ring: the tiles of its stretch in order, across segments ----
   uint8_t* ring = smem + S::RING + warp * STAGES * S::TILE;
   uint64_t* bar = bars + warp * STAGES;
-  Segment ps = locate(t0);
-  int p_seen = seen_by_last(ps);
-  int pt = t0 + warp;
+  // a copy is a page's part of the tile, or the tile: `per` copies a tile, `copy_shift` tokens each
+  const int copy_shift = min(a.c.page_shift, TK == 64 ? 6 : 5);
+  const int per = TK >> copy_shift;
+  Segment ps;
+  ps.first = w0;
+  ps.count = 0;
+  int p_seen = 0, p_tile = 0, p_end = 0;  // producer: next tile of its segment, and the first not its own
   int p_stage = 0, in_flight = 0;
-  uint32_t holds = 0;  // 2 bits per stage: which blocks of 16 tokens were fetched
-  int2 entry = make_int2(-1, -1);
-  int entry_at = 0;    // lane l has the table entries of tile entry_at + W l
+  uint32_t holds = 0;  // `per` bits per stage: which copies were made
+  int32_t entry = -1;  // lane l: table entry of copy entry_at + l
+  int entry_at = 0;
   bool entry_ok = false;
   const auto fetch = [&]() {
-    if (pt >= t1) return;
-    while (pt >= ps.first + ps.count) {
-      ps = locate(ps.first + ps.count);
+    while (p_tile >= p_end) {  // on to the next segment of the stretch
+      const int at = ps.first + ps.count;
+      if (at >= w1) return;
+      ps = locate(at);
       p_seen = seen_by_last(ps);
+      // unit 0 of a segment carries no keys; tiles behind the last row's keys are not needed
+      p_tile = max(at, w0) - ps.first - 1;
+      p_tile = max(p_tile, 0);
+      p_end = min(min(ps.first + ps.count, w1) - ps.first - 1, (p_seen + TK - 1) / TK);
       entry_ok = false;
     }
-    if (!entry_ok || pt - entry_at >= 32 * W) {
-      const int my = pt + W * lane;
-      entry = make_int2(-1, -1);
-      if (my < ps.first + ps.count) {
-        const int b0 = ((my - ps.first) * TK) >> a.c.page_shift, b1 = ((my - ps.first) * TK + 16) >> a.c.page_shift;
-        const int32_t* row = a.table + ps.b * a.table_stride;
-        if (b0 < a.max_blocks) entry.x = row[b0];
-        if (b1 < a.max_blocks) entry.y = b1 == b0 ? entry.x : row[b1];
-      }
-      entry_at = pt;
+    const int first = p_tile * per;
+    if (!entry_ok || first - entry_at >= 32) {
+      entry_at = first;
       entry_ok = true;
+      const int blk = (first + lane) << copy_shift >> a.c.page_shift;
+      entry = -1;
+      if (blk < a.max_blocks && ((first + lane) << copy_shift) < p_seen) entry = a.table[ps.b * a.table_stride + blk];
     }
-    const int from = (pt - entry_at) / W;
-    const int32_t page0 = __shfl_sync(0xffffffffu, entry.x, from), page1 = __shfl_sync(0xffffffffu, entry.y, from);
-    const int tok = (pt - ps.first) * TK;
-    const bool want0 = tok < p_seen, want1 = tok + 16 < p_seen;
-    const bool ok0 = want0 && page0 >= 0 && page0 < a.c.n_pages, ok1 = want1 && page1 >= 0 && page1 < a.c.n_pages;
-    if (lane == 0) {
-      if (want0 != ok0 || want1 != ok1) bad = 1;
-      const uint32_t dst = smem_addr(ring + p_stage * S::TILE);
-      uint64_t* br = bar + p_stage;
-      const int in_page = (tok & (a.c.page_tokens() - 1)) >> 4;
-      const uint8_t* s0 = a.c.pages + ((int64_t)page0 * a.c.Hkv + ps.h) * a.c.page_bytes + in_page * Blk::BYTES;
-      mbar_arrive_expect_tx(br, ((int)ok0 + (int)ok1) * Blk::BYTES);
-      if (ok0 && ok1 && a.c.page_shift > 4) {
-        bulk_load(dst, s0, 2 * Blk::BYTES, br);
-      } else {
-        if (ok0) bulk_load(dst, s0, Blk::BYTES, br);
-        if (ok1)
-          bulk_load(dst + Blk::BYTES,
-                    a.c.page_shift > 4 ? s0 + Blk::BYTES
-                                       : a.c.pages + ((int64_t)page1 * a.c.Hkv + ps.h) * a.c.page_bytes,
-                    Blk::BYTES, br);
-      }
-    }
-    holds = (holds & ~(3u << (2 * p_stage))) | (((uint32_t)ok0 | (uint32_t)ok1 << 1) << (2 * p_stage));
+    const int32_t page = __shfl_sync(0xffffffffu, entry, (first - entry_at + lane) & 31);
+    const int tok = (first + lane) << copy_shift;
+    const bool want = lane < per && tok < p_seen, ok = want && page >= 0 && page < a.c.n_pages;
+    if (want && !ok) bad = 1;
+    const uint32_t bytes = ok ? min(1 << copy_shift >> 4, (p_seen - tok + 15) >> 4) * Blk::BYTES : 0;
+    const uint32_t all = __reduce_add_sync(0xffffffffu, bytes), made = __ballot_sync(0xffffffffu, ok);
+    if (lane == 0) mbar_arrive_expect_tx(bar + p_stage, all);
+    __syncwarp();
+    if (ok)
+      bulk_load(smem_addr(ring + p_stage * S::TILE) + (lane << copy_shift >> 4) * Blk::BYTES,
+                a.c.pages + ((int64_t)page * a.c.Hkv + ps.h) * a.c.page_bytes +
+                    ((tok & (a.c.page_tokens() - 1)) >> 4) * Blk::BYTES,
+                bytes, bar + p_stage);
+    holds = (holds & ~(((1u << per) - 1) << (4 * p_stage))) | made << (4 * p_stage);
     p_stage = p_stage + 1 == STAGES ? 0 : p_stage + 1;
     ++in_flight;
-    pt += W;
+    ++p_tile;
   };
   for (int i = 0; i < STAGES; ++i) fetch();
 
   int c_stage = 0;
   uint32_t c_parity = 0;
-  int tile = t0 + warp;
   const int key_of = (g & 1) ? 4 + ((g >> 1) ^ 1) : g >> 1;  // key of operand row g, in 8
+  const auto weight = [](float x, float top) { return x == NEG_INF ? 0.f : ex2(x - top); };
+  const auto write_row = [&](const Segment& s, int r, int ch, float4 x, float top, float sum) {
+    const int rc = s.rt * ROWS + r, token = rc / a.group, hd = s.h * a.group + rc - token * a.group;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint2 w;
+    w.x = pack_bf16x2(x.x * inv, x.y * inv);
+    w.y = pack_bf16x2(x.z * inv, x.w * inv);
+    *reinterpret_cast<uint2*>(a.O + (int64_t)hd * a.o_head + (int64_t)(s.q0 + token) * a.o_row + ch) = w;
+    if (ch == 0 && a.lse)
+      a.lse[(int64_t)hd * a.total_q + s.q0 + token] = sum == 0.f ? NEG_INF : (top + log2f(sum)) * (1.f / LOG2E);
+  };
+  if (lane == 0) ends[warp] = 0;
 
-  for (int at = t0; at < t1;) {
+  for (int at = w0; at < w1;) {
     const Segment s = locate(at);
-    const int s_end = min(s.first + s.count, t1);
-    const int seen = min(seen_by_last(s), s.kv);
+    const int s_end = min(s.first + s.count, w1);
+    const int seen = seen_by_last(s);
     const int row0 = s.rt * ROWS, rows = min(ROWS, s.n * a.group - row0);
     const int seen_first = s.kv - s.n + row0 / a.group + 1;
 
@@ -369,153 +398,170 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
       }
     }
 
-    for (; tile < s_end; tile += W) {
-      const bool there = mbar_wait(bar + c_stage, c_parity, &abort_flag);
-      const uint8_t* kb = ring + c_stage * S::TILE;
-      const uint32_t have = there ? (holds >> (2 * c_stage)) & 3u : 0u;
-      const int tok = (tile - s.first) * TK;
-      if (have) {
-        // keys from here on are hidden from every row: behind the last row's, or on no page
-        const bool partial = have != 3u || tok + TK > min(seen_first, s.kv);
-        float sc[2][NT][4];
-        uint32_t vsw[2][2][NG];
-        float vmax = 0.f;
-        bool grow = false;
+    // One tile.  PARTIAL: some keys are hidden, from all rows (behind the last row's, or on no page)
+    // or from some.
+    const auto tile_pass = [&](auto partial_tag, const uint8_t* kb, int tok, uint32_t have) {
+      constexpr bool PARTIAL = decltype(partial_tag)::value;
+      float sc[MT][NT][4];
+      uint32_t vsw[MT][2][NG];
+      float vmax = 0.f, top[NT][2];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          const uint8_t* blk = kb + mt * Blk::BYTES;
-          const uint4 k0 = *reinterpret_cast<const uint4*>(blk + 64 * key_of + 16 * c);
-          const uint4 k1 = *reinterpret_cast<const uint4*>(blk + 64 * (key_of + 8) + 16 * c);
-          float acc[NG][NT][4];
+      for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = NEG_INF;
 #pragma unroll
-          for (int gr = 0; gr < NG; ++gr)
+      for (int mt = 0; mt < MT; ++mt) {
+        const uint8_t* blk = kb + mt * Blk::BYTES;
+        const uint4 k0 = *reinterpret_cast<const uint4*>(blk + 64 * key_of + 16 * c);
+        const uint4 k1 = *reinterpret_cast<const uint4*>(blk + 64 * (key_of + 8) + 16 * c);
+        float acc[NG][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+        for (int gr = 0; gr < NG; ++gr)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[gr][nt][e] = 0.f;
-          const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t u0 = w0[i] >> 8, u1 = w1[i] >> 8;
+            for (int e = 0; e < 4; ++e) acc[gr][nt][e] = 0.f;
+        const uint32_t x0[4] = {k0.x, k0.y, k0.z, k0.w}, x1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma16816(acc[i * NG / 4][nt], w0[i] & 0x000f000fu, w1[i] & 0x000f000fu, w0[i] & 0x00f000f0u,
-                       w1[i] & 0x00f000f0u, qf[nt][2 * i][0], qf[nt][2 * i][1]);
-              mma16816(acc[i * NG / 4][nt], u0 & 0x000f000fu, u1 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x00f000f0u,
-                       qf[nt][2 * i + 1][0], qf[nt][2 * i + 1][1]);
-            }
-          }
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t u0 = x0[i] >> 8, u1 = x1[i] >> 8;
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int key = tok + 16 * mt + 8 * r + key_of;
-            const bool shown = key < seen && ((have >> mt) & 1u);
-            uint32_t ksw[NG];
-            const uint32_t* kp = reinterpret_cast<const uint32_t*>(blk + Blk::K_SCALES + 4 * NG * (key_of + 8 * r));
-            const uint32_t* vp = reinterpret_cast<const uint32_t*>(blk + Blk::V_SCALES + 4 * NG * (key_of + 8 * r));
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-              ksw[gr] = kp[gr];
-              vsw[mt][r][gr] = vp[gr];
-              if (partial && !shown) ksw[gr] = 0, vsw[mt][r][gr] = 0;
-              vmax = fmaxf(vmax, bf_lo(vsw[mt][r][gr]));
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float x = 0.f;
-#pragma unroll
-                for (int gr = 0; gr < NG; ++gr)
-                  x = fmaf(acc[gr][nt][2 * r + e], bf_lo(ksw[gr]) * to_score, fmaf(bf_hi(ksw[gr]), qs[gr][nt][e], x));
-                if (partial && (!shown || key >= lim[nt][e])) x = NEG_INF;
-                sc[mt][nt][2 * r + e] = x;
-                grow |= x > m[nt][e] + 8.f;
-              }
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816(acc[i * NG / 4][nt], x0[i] & 0x000f000fu, x1[i] & 0x000f000fu, x0[i] & 0x00f000f0u,
+                     x1[i] & 0x00f000f0u, qf[nt][2 * i][0], qf[nt][2 * i][1]);
+            mma16816(acc[i * NG / 4][nt], u0 & 0x000f000fu, u1 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x00f000f0u,
+                     qf[nt][2 * i + 1][0], qf[nt][2 * i + 1][1]);
           }
         }
-        grow |= vmax > vtop;
-        if (__any_sync(0xffffffffu, grow)) {
-          // a score 2^8 above the running maximum (or a V step above every one before): the
-          // maximum is taken anew and what was summed so far is scaled down
 #pragma unroll
-          for (int off = 16; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
-          const float vnew = fmaxf(vtop, __uint_as_float((__float_as_uint(vmax) + 0x007fffffu) & 0x7f800000u));
-          const float fv = vtop * inv_pow2(vnew);
-          vtop = vnew;
+        for (int r = 0; r < 2; ++r) {
+          const int key = tok + 16 * mt + 8 * r + key_of;
+          const bool shown = !PARTIAL || (key < seen && ((have >> ((16 * mt) >> copy_shift)) & 1u));
+          uint32_t ksw[NG];
+          const uint32_t* kp = reinterpret_cast<const uint32_t*>(blk + Blk::K_SCALES + 4 * NG * (key_of + 8 * r));
+          const uint32_t* vp = reinterpret_cast<const uint32_t*>(blk + Blk::V_SCALES + 4 * NG * (key_of + 8 * r));
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) {
+            ksw[gr] = shown ? kp[gr] : 0u;
+            vsw[mt][r][gr] = shown ? vp[gr] : 0u;
+            vmax = fmaxf(vmax, bf_lo(vsw[mt][r][gr]));
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float x = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][2 + e]), fmaxf(sc[1][nt][e], sc[1][nt][2 + e]));
+              float x = 0.f;
 #pragma unroll
-              for (int off = 16; off > 2; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-              const float mn = fmaxf(m[nt][e], x);
-              const float f = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);
-              m[nt][e] = mn;
-              l[nt][e] *= f;
-#pragma unroll
-              for (int gr = 0; gr < NG; ++gr) z[gr][nt][e] *= f;
-#pragma unroll
-              for (int t = 0; t < 8; ++t) {
-                o[t][nt][e] *= f * fv;
-                o[t][nt][2 + e] *= f * fv;
-              }
+              for (int gr = 0; gr < NG; ++gr)
+                x = gr == 0 ? fmaf(acc[gr][nt][2 * r + e], bf_lo(ksw[gr]) * to_score, bf_hi(ksw[gr]) * qs[gr][nt][e])
+                            : fmaf(acc[gr][nt][2 * r + e], bf_lo(ksw[gr]) * to_score,
+                                   fmaf(bf_hi(ksw[gr]), qs[gr][nt][e], x));
+              if (PARTIAL && (!shown || key >= lim[nt][e])) x = NEG_INF;
+              sc[mt][nt][2 * r + e] = x;
+              top[nt][e] = fmaxf(top[nt][e], x);
             }
         }
-        const float vinv = 128.f * inv_pow2(vtop);
+      }
+      bool grow = vmax > vtop;
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          uint32_t pf[NG][NT][2];
+      for (int nt = 0; nt < NT; ++nt) grow |= top[nt][0] > m[nt][0] + 8.f || top[nt][1] > m[nt][1] + 8.f;
+      if (__any_sync(0xffffffffu, grow)) {
+        // a score 2^8 above the running maximum (or a V step above every one before): the maximum is
+        // taken anew and what was summed so far is scaled down
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float p[NT][2];
+        for (int off = 16; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
+        const float vnew = fmaxf(vtop, __uint_as_float((__float_as_uint(vmax) + 0x007fffffu) & 0x7f800000u));
+        const float fv = vtop * inv_pow2(vnew);
+        vtop = vnew;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                p[nt][e] = ex2(sc[mt][nt][2 * r + e] - (m[nt][e] == NEG_INF ? 0.f : m[nt][e]));
-                l[nt][e] += p[nt][e];
-              }
-            const int key = tok + 16 * mt + 8 * r + key_of;
+          for (int e = 0; e < 2; ++e) {
+            float x = top[nt][e];
 #pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-              const float vs = bf_lo(vsw[mt][r][gr]) * vinv, vz = bf_hi(vsw[mt][r][gr]);
+            for (int off = 16; off > 2; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+            const float mn = fmaxf(m[nt][e], x);
+            const float f = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);
+            m[nt][e] = mn;
+            l[nt][e] *= f;
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                float y[2];
+            for (int gr = 0; gr < NG; ++gr) z[gr][nt][e] *= f;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  // a key hidden from this row alone may hold NaN: no product with it
-                  const bool hidden = partial && key >= lim[nt][e];
-                  y[e] = hidden ? 0.f : p[nt][e] * vs;
-                  z[gr][nt][e] += hidden ? 0.f : p[nt][e] * vz;
-                }
-                pf[gr][nt][r] = transpose8x8(half2_bits(y[0], y[1]));
-              }
+            for (int t = 0; t < 8; ++t) {
+              o[t][nt][e] *= f * fv;
+              o[t][nt][2 + e] *= f * fv;
             }
           }
-          const uint8_t* vb = kb + mt * Blk::BYTES + Blk::V_CODES;
-          uint2 v[4];
+      }
+      const float vinv = 128.f * inv_pow2(vtop);
+      float base[NT][2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // keys 2c, 2c + 1, 2c + 8, 2c + 9 of the operand
-            const int key = ((i & 1) ? 4 + (c ^ 1) : c) + 8 * (i >> 1);
-            v[i] = *reinterpret_cast<const uint2*>(vb + 64 * key + 8 * (g ^ kv4_v_swizzle(key)));
-          }
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t sel = (q & 1) ? 0x7632u : 0x5410u;
-            const uint32_t x = (q >> 1) ? __byte_perm(v[0].y, v[1].y, sel) : __byte_perm(v[0].x, v[1].x, sel);
-            const uint32_t y = (q >> 1) ? __byte_perm(v[2].y, v[3].y, sel) : __byte_perm(v[2].x, v[3].x, sel);
-            const uint32_t x8 = x >> 8, y8 = y >> 8;
+        for (int e = 0; e < 2; ++e) base[nt][e] = m[nt][e] == NEG_INF ? 0.f : m[nt][e];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        uint32_t pf[NG][NT][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float p[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              p[nt][e] = ex2(sc[mt][nt][2 * r + e] - base[nt][e]);
+              l[nt][e] += p[nt][e];
+            }
+          const int key = tok + 16 * mt + 8 * r + key_of;
+#pragma unroll
+          for (int gr = 0; gr < NG; ++gr) {
+            const float step = bf_lo(vsw[mt][r][gr]), vs = step * vinv;
+            const float vz = fmaf(8.f, step, bf_hi(vsw[mt][r][gr]));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const uint32_t b0 = pf[q * NG / 4][nt][0], b1 = pf[q * NG / 4][nt][1];
-              mma16816(o[2 * q][nt], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u, b0, b1);
-              mma16816(o[2 * q + 1][nt], x8 & 0x000f000fu, x8 & 0x00f000f0u, y8 & 0x000f000fu, y8 & 0x00f000f0u, b0, b1);
+              float y[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                // a key hidden from this row alone may hold NaN: no product with it
+                const bool hidden = PARTIAL && key >= lim[nt][e];
+                y[e] = hidden ? 0.f : p[nt][e] * vs;
+                z[gr][nt][e] = hidden ? z[gr][nt][e] : fmaf(p[nt][e], vz, z[gr][nt][e]);
+              }
+              pf[gr][nt][r] = transpose8x8(half2_bits(y[0], y[1]));
             }
+          }
+        }
+        const uint8_t* vb = kb + mt * Blk::BYTES + Blk::V_CODES;
+        uint2 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // keys 2c, 2c + 1, 2c + 8, 2c + 9 of the operand
+          const int key = ((i & 1) ? 4 + (c ^ 1) : c) + 8 * (i >> 1);
+          v[i] = *reinterpret_cast<const uint2*>(vb + 64 * key + 8 * (g ^ kv4_v_swizzle(key)));
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t sel = (q & 1) ? 0x7632u : 0x5410u;
+          const uint32_t x = (q >> 1) ? __byte_perm(v[0].y, v[1].y, sel) : __byte_perm(v[0].x, v[1].x, sel);
+          const uint32_t y = (q >> 1) ? __byte_perm(v[2].y, v[3].y, sel) : __byte_perm(v[2].x, v[3].x, sel);
+          const uint32_t x8 = x >> 8, y8 = y >> 8;
+          const uint32_t a00 = centred_lo(x), a01 = centred_hi(x), a02 = centred_lo(y), a03 = centred_hi(y);
+          const uint32_t a10 = centred_lo(x8), a11 = centred_hi(x8), a12 = centred_lo(y8), a13 = centred_hi(y8);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t b0 = pf[q * NG / 4][nt][0], b1 = pf[q * NG / 4][nt][1];
+            mma16816(o[2 * q][nt], a00, a01, a02, a03, b0, b1);
+            mma16816(o[2 * q + 1][nt], a10, a11, a12, a13, b0, b1);
           }
         }
       }
+    };
+
+    const int tiles = min(s_end - s.first - 1, (seen + TK - 1) / TK);
+    for (int tile = max(at - s.first - 1, 0); tile < tiles; ++tile) {
+      const bool there = mbar_wait(bar + c_stage, c_parity, &abort_flag);
+      const uint8_t* kb = ring + c_stage * S::TILE;
+      const uint32_t all = (1u << per) - 1, have = there ? (holds >> (4 * c_stage)) & all : 0u;
+      const int tok = tile * TK;
+      if (have == all && tok + TK <= seen_first) tile_pass(std::false_type{}, kb, tok, have);
+      else if (have) tile_pass(std::true_type{}, kb, tok, have);
       __syncwarp();  // every lane has read the stage
       --in_flight;
       if (++c_stage == STAGES) c_stage = 0, c_parity ^= 1;
@@ -533,121 +579,40 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) z[gr][nt][e] += __shfl_xor_sync(0xffffffffu, z[gr][nt][e], off);
         }
-    const float of = vtop * 131072.f;  // 2^24 / 2^7
+    const float of = vtop * 0.0078125f;  // 1 / 128
+    const bool starts = s.first >= w0, stops = s.first + s.count <= w1;
+    // a head (it began in a stretch before) goes to its own place, a tail into the ring, which is
+    // empty then: a tail is a stretch's last segment
+    float* mine = starts ? reinterpret_cast<float*>(ring) : heads + warp * ROWS * HD;
+    float* mine_st = stats + (2 * warp + (starts ? 1 : 0)) * ROWS * 2;
 #pragma unroll
-    for (int t = 0; t < 8; ++t)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int e = 0; e < 2; ++e) {
+        const int r = nt * 8 + 2 * c + e;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          o[t][nt][e] = fmaf(o[t][nt][e], of, z[(t >> 1) * NG / 4][nt][e]);
-          o[t][nt][2 + e] = fmaf(o[t][nt][2 + e], of * 0.0625f, z[(t >> 1) * NG / 4][nt][e]);
-        }
-    const auto weight = [](float x, float top) { return x == NEG_INF ? 0.f : ex2(x - top); };
-    const int slot = warp & (S::JOIN - 1);
-    for (int half = 1; half >= 0; --half) {
-      if (warp / S::JOIN == half) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = nt * 8 + 2 * c + e;
-            float* row = join + (slot * ROWS + r) * HD;
-            float* st = stat + (slot * ROWS + r) * 2;
-            float f = 1.f, f2 = 0.f;
-            if (half == 0) {  // the other half's rows are there: add them
-              const float m2 = st[0], l2 = st[1], mn = fmaxf(m[nt][e], m2);
-              f = weight(m[nt][e], mn);
-              f2 = weight(m2, mn);
-              m[nt][e] = mn;
-              l[nt][e] = l[nt][e] * f + l2 * f2;
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float4* d = reinterpret_cast<float4*>(row + 32 * q + 4 * g);
-              float4 x = make_float4(o[2 * q][nt][e] * f, o[2 * q][nt][2 + e] * f, o[2 * q + 1][nt][e] * f,
-                                     o[2 * q + 1][nt][2 + e] * f);
-              if (half == 0) {
-                const float4 y = *d;
-                x.x = fmaf(y.x, f2, x.x), x.y = fmaf(y.y, f2, x.y), x.z = fmaf(y.z, f2, x.z), x.w = fmaf(y.w, f2, x.w);
-              }
-              *d = x;
-            }
-            __syncwarp();  // the row's statistics were read by every lane of it
-            if (g == 0) st[0] = m[nt][e], st[1] = l[nt][e];
+        for (int q = 0; q < 4; ++q) {
+          const float zq = z[q * NG / 4][nt][e];
+          const float4 x = make_float4(fmaf(o[2 * q][nt][e], of, zq), fmaf(o[2 * q][nt][2 + e], of * 0.0625f, zq),
+                                       fmaf(o[2 * q + 1][nt][e], of, zq),
+                                       fmaf(o[2 * q + 1][nt][2 + e], of * 0.0625f, zq));
+          if (starts && stops) {
+            if (r < rows) write_row(s, r, 32 * q + 4 * g, x, m[nt][e], l[nt][e]);
+          } else {
+            *reinterpret_cast<float4*>(mine + r * HD + 32 * q + 4 * g) = x;
           }
-      }
-      __syncthreads();
-    }
-
-    // ---- the CTA's rows, to O or to the workspace ----
-    const bool whole = s.first >= t0 && s.first + s.count <= t1;
-    const auto write_row = [&](int r, int ch, float4 x, float top, float sum) {
-      const int rc = row0 + r, token = rc / a.group, hd = s.h * a.group + rc - token * a.group;
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      uint2 w;
-      w.x = pack_bf16x2(x.x * inv, x.y * inv);
-      w.y = pack_bf16x2(x.z * inv, x.w * inv);
-      *reinterpret_cast<uint2*>(a.O + (int64_t)hd * a.o_head + (int64_t)(s.q0 + token) * a.o_row + ch) = w;
-      if (ch == 0 && a.lse)
-        a.lse[(int64_t)hd * a.total_q + s.q0 + token] = sum == 0.f ? NEG_INF : (top + log2f(sum)) * (1.f / LOG2E);
-    };
-    float* mine = a.partial + (2 * (int64_t)blockIdx.x + (s.first >= t0 ? 1 : 0)) * MAX_ROWS * PART;
-    for (int i = tid; i < rows * (HD / 4); i += THREADS) {
-      const int r = i / (HD / 4), ch = (i % (HD / 4)) * 4;
-      float top = NEG_INF, sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < S::JOIN; ++j) top = fmaxf(top, stat[(j * ROWS + r) * 2]);
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int j = 0; j < S::JOIN; ++j) {
-        const float f = weight(stat[(j * ROWS + r) * 2], top);
-        const float4 y = *reinterpret_cast<const float4*>(join + (j * ROWS + r) * HD + ch);
-        sum = fmaf(stat[(j * ROWS + r) * 2 + 1], f, sum);
-        x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
-      }
-      if (whole) {
-        write_row(r, ch, x, top, sum);
-      } else {
-        *reinterpret_cast<float4*>(mine + r * HD + ch) = x;
-        if (ch == 0) {
-          mine[MAX_ROWS * HD + 2 * r] = top;
-          mine[MAX_ROWS * HD + 2 * r + 1] = sum;
         }
+        if (!(starts && stops) && g == 0) mine_st[2 * r] = m[nt][e], mine_st[2 * r + 1] = l[nt][e];
+      }
+    if (lane == 0) {
+      if (!starts) {
+        ends[warp] |= stops ? 3 : 1;
+        if (w0 == t0) segs[W] = s;
+      } else if (!stops) {
+        ends[warp] |= 4;
+        segs[warp] = s;
       }
     }
-    if (!whole) {
-      const auto owner = [&](int t) { return (int)((((int64_t)t + 1) * active - 1) / total); };
-      const int from = owner(s.first), to = owner(s.first + s.count - 1);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        arrived_last = atomicAdd(a.arrivals + from, 1u) == (uint32_t)(to - from);
-        if (arrived_last) a.arrivals[from] = 0;  // ready for the next launch
-        __threadfence();
-      }
-      __syncthreads();
-      if (arrived_last) {
-        const auto part = [&](int i) { return a.partial + (2 * (int64_t)i + (i == from ? 1 : 0)) * MAX_ROWS * PART; };
-        for (int i = tid; i < rows * (HD / 4); i += THREADS) {
-          const int r = i / (HD / 4), ch = (i % (HD / 4)) * 4;
-          float top = NEG_INF, sum = 0.f;
-          for (int k = from; k <= to; ++k) top = fmaxf(top, __ldcg(part(k) + MAX_ROWS * HD + 2 * r));
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int k = from; k <= to; ++k) {
-            const float* p = part(k);
-            const float2 st = __ldcg(reinterpret_cast<const float2*>(p + MAX_ROWS * HD + 2 * r));
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(p + r * HD + ch));
-            const float f = weight(st.x, top);
-            sum = fmaf(st.y, f, sum);
-            x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
-          }
-          write_row(r, ch, x, top, sum);
-        }
-      }
-    }
-    __syncthreads();  // join and stat are free again
     at = s_end;
   }
   // nothing is in flight here unless a wait gave up: let what was issued land
@@ -657,35 +622,122 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
     if (++c_stage == STAGES) c_stage = 0, c_parity ^= 1;
   }
   __syncthreads();
+
+  // ---- segments over several warps: a chain is the tail (or the CTA's head) and the heads after it ----
+  const auto part = [&](int i, int which) { return a.partial + (2 * (int64_t)i + which) * MAX_ROWS * PART; };
+  const auto owner = [&](int t) { return (int)((((int64_t)t + 1) * active - 1) / total); };
+  uint32_t crosses = 0;  // bit 0: the CTA's head, bit 1: its tail, in the workspace
+  Segment cross_seg[2];
+  int lead = 0;  // the first warp with a stretch
+  while ((int64_t)(t1 - t0) * (lead + 1) / W == 0) ++lead;
+  for (int first = -1; first < W; ++first) {
+    if (first < 0 ? !(ends[lead] & 1) : !(ends[first] & 4)) continue;
+    const Segment s = segs[first < 0 ? W : first];
+    int last = first < 0 ? lead : first;
+    bool open = first >= 0 || !(ends[lead] & 2);
+    for (int w = last + 1; w < W && open; ++w) {
+      if (!(ends[w] & 1)) continue;  // a warp without a stretch
+      last = w;
+      open = !(ends[w] & 2);
+    }
+    const bool whole = s.first >= t0 && s.first + s.count <= t1;
+    const int which = s.first >= t0 ? 1 : 0, rows = min(ROWS, s.n * a.group - s.rt * ROWS);
+    for (int i = tid; i < rows * (HD / 4); i += THREADS) {
+      const int r = i / (HD / 4), ch = (i % (HD / 4)) * 4;
+      const auto member = [&](int w) { return stats + (2 * w + (w == first ? 1 : 0)) * ROWS * 2 + 2 * r; };
+      const auto is_in = [&](int w) { return w == first || (ends[w] & 1); };
+      float top = NEG_INF, sum = 0.f;
+      for (int w = max(first, 0); w <= last; ++w)
+        if (is_in(w)) top = fmaxf(top, member(w)[0]);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = max(first, 0); w <= last; ++w) {
+        if (!is_in(w)) continue;
+        const float* src = w == first ? reinterpret_cast<const float*>(smem + S::RING + w * STAGES * S::TILE) : heads + w * ROWS * HD;
+        const float4 y = *reinterpret_cast<const float4*>(src + r * HD + ch);
+        const float f = weight(member(w)[0], top);
+        sum = fmaf(member(w)[1], f, sum);
+        x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
+      }
+      if (whole) {
+        write_row(s, r, ch, x, top, sum);
+      } else {
+        float* dst = part(blockIdx.x, which);
+        *reinterpret_cast<float4*>(dst + r * HD + ch) = x;
+        if (ch == 0) *reinterpret_cast<float2*>(dst + MAX_ROWS * HD + 2 * r) = make_float2(top, sum);
+      }
+    }
+    if (!whole) {
+      crosses |= 1u << which;
+      cross_seg[which] = s;
+    }
+  }
+
+  // ---- segments over several CTAs: joined by the one that arrives last ----
+  if (crosses) {
+    __threadfence();
+    __syncthreads();
+    if (tid < 2 && (crosses >> tid & 1)) {
+      const Segment& s = cross_seg[tid];
+      const int from = owner(s.first), to = owner(s.first + s.count - 1);
+      last_of[tid] = atomicAdd(a.arrivals + from, 1u) == (uint32_t)(to - from);
+      if (last_of[tid]) a.arrivals[from] = 0;  // ready for the next launch
+      __threadfence();
+    }
+    __syncthreads();
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      if (!(crosses >> which & 1) || !last_of[which]) continue;
+      const Segment s = cross_seg[which];
+      const int from = owner(s.first), to = owner(s.first + s.count - 1);
+      const int rows = min(ROWS, s.n * a.group - s.rt * ROWS);
+      for (int i = tid; i < rows * (HD / 4); i += THREADS) {
+        const int r = i / (HD / 4), ch = (i % (HD / 4)) * 4;
+        float top = NEG_INF, sum = 0.f;
+#pragma unroll 8
+        for (int k = from; k <= to; ++k) top = fmaxf(top, __ldcg(part(k, k == from) + MAX_ROWS * HD + 2 * r));
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = from; k <= to; ++k) {
+          const float* p = part(k, k == from);
+          const float2 st = __ldcg(reinterpret_cast<const float2*>(p + MAX_ROWS * HD + 2 * r));
+          const float4 y = __ldcg(reinterpret_cast<const float4*>(p + r * HD + ch));
+          const float f = weight(st.x, top);
+          sum = fmaf(st.y, f, sum);
+          x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
+        }
+        write_row(s, r, ch, x, top, sum);
+      }
+    }
+  }
   if (tid == 0) {
     if (abort_flag) atomicOr(a.c.state, DEV_ERR_TIMEOUT);
     if (bad) atomicOr(a.c.state, DEV_ERR_BOUNDS);
   }
 }
 
-template <int NG, int NT, int W, int STAGES>
+template <int NG, int NT, int TK, int W, int STAGES>
 cudaError_t launch(const AttendArgs& a, int dev, cudaStream_t st) {
-  using S = AttendSmem<NG, NT, W, STAGES>;
+  using S = AttendSmem<NG, NT, TK, W, STAGES>;
   static_assert(S::CUM + (KV4_MAX_B + 1) * 4 <= 226 * 1024, "shared memory of one CTA");
   static_assert(8 * NT <= MAX_ROWS, "rows of a partial result");
   static std::atomic<uint64_t> ready{0};
   if (device_pending(ready, dev)) {
-    const cudaError_t e = cudaFuncSetAttribute(kv4_attend_kernel<NG, NT, W, STAGES>,
+    const cudaError_t e = cudaFuncSetAttribute(kv4_attend_kernel<NG, NT, TK, W, STAGES>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                S::CUM + (KV4_MAX_B + 1) * 4);
     if (e != cudaSuccess) return e;
     mark_device(ready, dev);
   }
   count_launches(1);
-  kv4_attend_kernel<NG, NT, W, STAGES>
+  kv4_attend_kernel<NG, NT, TK, W, STAGES>
       <<<std::min(sm_count(), MAX_CTAS), W * 32, S::CUM + (a.B + 1) * 4, st>>>(a);
   return cudaGetLastError();
 }
 
 template <int NG>
 cudaError_t launch_rows(const AttendArgs& a, int max_q, int dev, cudaStream_t st) {
-  if ((int64_t)max_q * a.group <= 8) return launch<NG, 1, 16, 2>(a, dev, st);
-  return launch<NG, 2, 8, 4>(a, dev, st);
+  if ((int64_t)max_q * a.group <= 8) return launch<NG, 1, 64, 8, 2>(a, dev, st);
+  return launch<NG, 2, 32, 8, 3>(a, dev, st);
 }
 
 constexpr size_t ARRIVALS_BYTES = 1024;

@@ -147,7 +147,7 @@ def attend(pages, page, group, Q, table, kv_lens, cu_q, scale, hidden=lambda b, 
             K, V, Ka, Va, St = np.zeros((kv, D)), np.zeros((kv, D)), np.zeros((kv, D)), np.zeros((kv, D)), 0.0
             for j, ((kc, ks, kl), (vc, vs, vl)) in enumerate(ps):
                 K[j], V[j] = kl + kc * ks, vl + vc * vs
-                Ka[j], Va[j] = np.abs(kl) + kc * ks, np.abs(vl) + vc * vs
+                Ka[j], Va[j] = np.abs(kl) + kc * ks, np.abs(vl + 8 * vs) + 8 * vs
                 St = max(St, float(np.nanmax(vs)) if not np.isnan(vs).all() else 0.0)
             for g in range(G):
                 for i in range(n):
@@ -173,6 +173,7 @@ def tolerance(O, lse, p, Va, reach, n, step):
     `reach` (the largest sum of magnitudes behind a score) * 136 * 2^-24 <= reach * 2^-16.
     Probabilities enter the second product in fp16 after the running maximum and the largest step are
     taken out: 2^-11 relative, or 2^-32 of the largest step (fp16's subnormals, at most 15 codes).
+    The second product runs on codes less 8, beside sums of lo + 8 step: their magnitudes are Va.
     A relative error of every weight moves O by at most twice its weighted magnitudes (numerator and
     denominator); sums over n weights in fp32 add n / 8 * 2^-24 (a thread sums every eighth key or
     fewer) and the exponential 2^-21.  O is rounded to bf16: 2^-8."""
