@@ -280,78 +280,107 @@ __device__ __forceinline__ uint32_t bf_pack(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // Eight channels of a row (lane l of 16: channels 8 l .. 8 l + 7) to eight codes in channel order,
-// and the group's (step, lo) word.  The product (x - lo) * r is rounded to a whole number in one
-// step, by adding 1.5 * 2^23 in the same fused operation: a value next to a border falls on its own
-// side, as it would in 64 bits.
+// and the group's (step, lo) word.  Smallest and largest value are found together, as the smallest
+// of x and of -x in the two halves of a word; a NaN in either is kept.  The product (x - lo) * r is
+// rounded to a whole number in one step, by adding 1.5 * 2^23 in the same fused operation: a value
+// next to a border falls on its own side, as it would in 64 bits.
 template <int NG>
 __device__ __forceinline__ uint32_t quantise8(const uint4& v, uint32_t& scale_word) {
-  float x[8];
-  x[0] = bf_lo(v.x), x[1] = bf_hi(v.x), x[2] = bf_lo(v.y), x[3] = bf_hi(v.y);
-  x[4] = bf_lo(v.z), x[5] = bf_hi(v.z), x[6] = bf_lo(v.w), x[7] = bf_hi(v.w);
-  float lo = x[0], hi = x[0], nan = 0.f;
+  constexpr uint32_t SIGNS = 0x80008000u;
+  const uint32_t lo2 = min2_nan(min2_nan(v.x, v.y), min2_nan(v.z, v.w));
+  const uint32_t hi2 = min2_nan(min2_nan(v.x ^ SIGNS, v.y ^ SIGNS), min2_nan(v.z ^ SIGNS, v.w ^ SIGNS));
+  uint32_t both = min2_nan(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));  // low half lo, high half -hi
 #pragma unroll
-  for (int e = 1; e < 8; ++e) lo = fminf(lo, x[e]), hi = fmaxf(hi, x[e]);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) nan += x[e] * 0.f;  // 0, or NaN if any is not finite
-#pragma unroll
-  for (int o = 8 / NG; o > 0; o >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    nan += __shfl_xor_sync(0xffffffffu, nan, o);
-  }
-  const float range = hi - lo;
-  float step = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(range, 15.f)));
+  for (int o = 8 / NG; o > 0; o >>= 1) both = min2_nan(both, __shfl_xor_sync(0xffffffffu, both, o));
+  const float lo = bf_lo(both), range = -bf_hi(both) - lo;
+  // range / 15, correctly rounded: a product with the rounded reciprocal and one correction by the
+  // exact remainder (Markstein, 1990)
+  const float q0 = range * (1.f / 15.f);
+  const float q = fmaf(fmaf(-15.f, q0, range), 1.f / 15.f, q0);
+  float step = __bfloat162float(__float2bfloat16_rn(q));
   if (step < 0x1p-126f) step = 0.f;
-  const float r = step > 0.f ? __fdiv_rn(1.f, step) : 0.f;
-  uint32_t code = 0;
+  const float r = step > 0.f ? __frcp_rn(step) : 0.f;
+  const float x[8] = {bf_lo(v.x), bf_hi(v.x), bf_lo(v.y), bf_hi(v.y), bf_lo(v.z), bf_hi(v.z), bf_lo(v.w), bf_hi(v.w)};
+  // a code is the low bits of the sum (no larger than 15: step is within 2^-9 of range / 15, so the
+  // largest product is below 15.06); shifted sums added up hold the codes and a constant
+  uint32_t code = 0u - 0x4b400000u * 0x11111111u;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float m = fmaf(__fsub_rn(x[e], lo), r, 12582912.f);
-    code |= min(__float_as_uint(m) - 0x4b400000u, 15u) << (4 * e);
-  }
+  for (int e = 0; e < 8; ++e) code += __float_as_uint(fmaf(__fsub_rn(x[e], lo), r, 12582912.f)) << (4 * e);
   scale_word = (__float_as_uint(step) >> 16) | (__float_as_uint(lo) & 0xffff0000u);
-  if (!(nan == 0.f) || !(range < __int_as_float(0x7f800000))) scale_word = 0x7fc07fc0u, code = 0;
+  if (!(range < __int_as_float(0x7f800000))) scale_word = 0x7fc07fc0u, code = 0;
   return code;
 }
 
-// Sixteen lanes take one (token, KV head): 16 bytes of K and of V each.  Bound by HBM: 512 bytes
-// read and 2 (64 + 4 NG) written per row.
+// Sixteen lanes take one (token, KV head) row, 16 bytes of K and of V each, ROW_UNROLL rows of
+// neighbouring tokens in flight.
+constexpr int ROW_UNROLL = 4;
+
+// The rows of a group: one head, ROW_UNROLL neighbouring tokens; a warp's two groups have neighbouring
+// heads.  Their slots, -1 where there is nothing to do.
+__device__ __forceinline__ void row_item(const RowArgs& a, int64_t& t0, int& h, int64_t (&slot)[ROW_UNROLL]) {
+  const int64_t item = (int64_t)blockIdx.x * (ROW_THREADS / 16) + (threadIdx.x >> 4);
+  const int64_t quad = item / a.c.Hkv;
+  h = (int)(item - quad * a.c.Hkv);
+  t0 = quad * ROW_UNROLL;
+#pragma unroll
+  for (int u = 0; u < ROW_UNROLL; ++u) {
+    slot[u] = t0 + u < a.T ? a.slots[t0 + u] : -1;
+    if (slot[u] >= a.c.n_slots()) {
+      if ((threadIdx.x & 15) == 0) atomicOr(a.c.state, DEV_ERR_BOUNDS);
+      slot[u] = -1;
+    }
+  }
+}
+
+template <int NG>
+__device__ __forceinline__ uint8_t* row_block(const Kv4View& c, int64_t slot, int h) {
+  return c.pages + ((slot >> c.page_shift) * c.Hkv + h) * c.page_bytes +
+         ((slot & (c.page_tokens() - 1)) >> 4) * Kv4Block<NG>::BYTES;
+}
+
+// Bound by HBM: 512 bytes read and 2 (64 + 4 NG) written per row.
 template <int NG>
 __global__ void __launch_bounds__(ROW_THREADS) kv4_append_kernel(const RowArgs a) {
   using Blk = Kv4Block<NG>;
   const int l = threadIdx.x & 15;
-  const int64_t item = (int64_t)blockIdx.x * (ROW_THREADS / 16) + (threadIdx.x >> 4);
-  const int64_t t = item / a.c.Hkv;
-  const int h = (int)(item - t * a.c.Hkv);
-  int64_t slot = -1;
-  if (t < a.T) slot = a.slots[t];
-  if (slot >= a.c.n_slots()) {
-    if (l == 0) atomicOr(a.c.state, DEV_ERR_BOUNDS);
-    slot = -1;
+  int64_t t0, slot[ROW_UNROLL];
+  int h;
+  row_item(a, t0, h, slot);
+  uint4 kx[ROW_UNROLL], vx[ROW_UNROLL];
+#pragma unroll
+  for (int u = 0; u < ROW_UNROLL; ++u) {
+    kx[u] = vx[u] = make_uint4(0, 0, 0, 0);
+    if (slot[u] >= 0) {
+      kx[u] = *reinterpret_cast<const uint4*>(a.K + h * a.k_head + (t0 + u) * a.k_row + l * 8);
+      vx[u] = *reinterpret_cast<const uint4*>(a.V + h * a.v_head + (t0 + u) * a.v_row + l * 8);
+    }
   }
-  uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
-  if (slot >= 0) {
-    kx = *reinterpret_cast<const uint4*>(a.K + h * a.k_head + t * a.k_row + l * 8);
-    vx = *reinterpret_cast<const uint4*>(a.V + h * a.v_head + t * a.v_row + l * 8);
-  }
-  uint32_t ks, vs;
-  const uint32_t kc = quantise8<NG>(kx, ks), vc = quantise8<NG>(vx, vs);
-  // V words hold four channels of two neighbouring quarters of the row (lanes l and l ^ 4): each
-  // lane hands over the half that its partner stores
   const int q = l >> 2, g = 2 * (l & 3) + (q & 1);
-  const uint32_t other = __shfl_xor_sync(0xffffffffu, vc, 4);
-  const uint32_t vw = (q & 1) ? __byte_perm(other, vc, 0x7632) : __byte_perm(vc, other, 0x5410);
-  if (slot < 0) return;
-  const int i = (int)(slot & 15);
-  uint8_t* blk = a.c.pages + ((slot >> a.c.page_shift) * a.c.Hkv + h) * a.c.page_bytes +
-                 ((slot & (a.c.page_tokens() - 1)) >> 4) * Blk::BYTES;
-  *reinterpret_cast<uint32_t*>(blk + 64 * i + 16 * (l & 3) + 4 * (l >> 2)) = kc;
-  *reinterpret_cast<uint32_t*>(blk + Blk::V_CODES + 64 * i + 8 * (g ^ kv4_v_swizzle(i)) + 4 * (q >> 1)) = vw;
-  if (l % (16 / NG) == 0) {
-    const int grp = l / (16 / NG);
-    *reinterpret_cast<uint32_t*>(blk + Blk::K_SCALES + 4 * NG * i + 4 * grp) = ks;
-    *reinterpret_cast<uint32_t*>(blk + Blk::V_SCALES + 4 * NG * i + 4 * grp) = vs;
+#pragma unroll
+  for (int u = 0; u < ROW_UNROLL; ++u) {
+    uint32_t ks, vs;
+    const uint32_t kc = quantise8<NG>(kx[u], ks), vc = quantise8<NG>(vx[u], vs);
+    // V words hold four channels of two neighbouring quarters of the row (lanes l and l ^ 4): each
+    // lane hands over the half that its partner stores
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, vc, 4);
+    const uint32_t vw = (q & 1) ? __byte_perm(other, vc, 0x7632) : __byte_perm(vc, other, 0x5410);
+    if (slot[u] < 0) continue;
+    const int i = (int)(slot[u] & 15);
+    uint8_t* blk = row_block<NG>(a.c, slot[u], h);
+    *reinterpret_cast<uint32_t*>(blk + 64 * i + 16 * (l & 3) + 4 * (l >> 2)) = kc;
+    *reinterpret_cast<uint32_t*>(blk + Blk::V_CODES + 64 * i + 8 * (g ^ kv4_v_swizzle(i)) + 4 * (q >> 1)) = vw;
+    if (l % (16 / NG) == 0) {
+      const int grp = l / (16 / NG);
+      *reinterpret_cast<uint32_t*>(blk + Blk::K_SCALES + 4 * NG * i + 4 * grp) = ks;
+      *reinterpret_cast<uint32_t*>(blk + Blk::V_SCALES + 4 * NG * i + 4 * grp) = vs;
+    }
   }
 }
 
@@ -359,40 +388,40 @@ __device__ __forceinline__ uint4 dequantise8(uint32_t code, uint32_t scale_word)
   const float step = bf_lo(scale_word), lo = bf_hi(scale_word);
   float x[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = fmaf((float)((code >> (4 * e)) & 15u), step, lo);
+  for (int e = 0; e < 8; ++e)  // 2^23 + code, less 2^23
+    x[e] = fmaf(__uint_as_float(((code >> (4 * e)) & 15u) | 0x4b000000u) - 8388608.f, step, lo);
   return make_uint4(bf_pack(x[0], x[1]), bf_pack(x[2], x[3]), bf_pack(x[4], x[5]), bf_pack(x[6], x[7]));
 }
 
+// Bound by HBM: the append's bytes the other way round.
 template <int NG>
 __global__ void __launch_bounds__(ROW_THREADS) kv4_read_kernel(const RowArgs a) {
   using Blk = Kv4Block<NG>;
   const int l = threadIdx.x & 15;
-  const int64_t item = (int64_t)blockIdx.x * (ROW_THREADS / 16) + (threadIdx.x >> 4);
-  const int64_t t = item / a.c.Hkv;
-  const int h = (int)(item - t * a.c.Hkv);
-  int64_t slot = -1;
-  if (t < a.T) slot = a.slots[t];
-  if (slot >= a.c.n_slots()) {
-    if (l == 0) atomicOr(a.c.state, DEV_ERR_BOUNDS);
-    slot = -1;
+  int64_t t0, slot[ROW_UNROLL];
+  int h;
+  row_item(a, t0, h, slot);
+  const int q = l >> 2, g = 2 * (l & 3) + (q & 1), grp = l / (16 / NG);
+  uint32_t kc[ROW_UNROLL], vw[ROW_UNROLL], ks[ROW_UNROLL], vs[ROW_UNROLL];
+#pragma unroll
+  for (int u = 0; u < ROW_UNROLL; ++u) {
+    kc[u] = vw[u] = ks[u] = vs[u] = 0;
+    if (slot[u] < 0) continue;
+    const int i = (int)(slot[u] & 15);
+    const uint8_t* blk = row_block<NG>(a.c, slot[u], h);
+    kc[u] = *reinterpret_cast<const uint32_t*>(blk + 64 * i + 16 * (l & 3) + 4 * (l >> 2));
+    vw[u] = *reinterpret_cast<const uint32_t*>(blk + Blk::V_CODES + 64 * i + 8 * (g ^ kv4_v_swizzle(i)) + 4 * (q >> 1));
+    ks[u] = *reinterpret_cast<const uint32_t*>(blk + Blk::K_SCALES + 4 * NG * i + 4 * grp);
+    vs[u] = *reinterpret_cast<const uint32_t*>(blk + Blk::V_SCALES + 4 * NG * i + 4 * grp);
   }
-  const int q = l >> 2, g = 2 * (l & 3) + (q & 1);
-  uint32_t kc = 0, vw = 0, ks = 0, vs = 0;
-  if (slot >= 0) {
-    const int i = (int)(slot & 15);
-    const uint8_t* blk = a.c.pages + ((slot >> a.c.page_shift) * a.c.Hkv + h) * a.c.page_bytes +
-                         ((slot & (a.c.page_tokens() - 1)) >> 4) * Blk::BYTES;
-    kc = *reinterpret_cast<const uint32_t*>(blk + 64 * i + 16 * (l & 3) + 4 * (l >> 2));
-    vw = *reinterpret_cast<const uint32_t*>(blk + Blk::V_CODES + 64 * i + 8 * (g ^ kv4_v_swizzle(i)) + 4 * (q >> 1));
-    const int grp = l / (16 / NG);
-    ks = *reinterpret_cast<const uint32_t*>(blk + Blk::K_SCALES + 4 * NG * i + 4 * grp);
-    vs = *reinterpret_cast<const uint32_t*>(blk + Blk::V_SCALES + 4 * NG * i + 4 * grp);
+#pragma unroll
+  for (int u = 0; u < ROW_UNROLL; ++u) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, vw[u], 4);
+    const uint32_t vc = (q & 1) ? __byte_perm(other, vw[u], 0x7632) : __byte_perm(vw[u], other, 0x5410);
+    if (slot[u] < 0) continue;
+    *reinterpret_cast<uint4*>(a.K + h * a.k_head + (t0 + u) * a.k_row + l * 8) = dequantise8(kc[u], ks[u]);
+    *reinterpret_cast<uint4*>(a.V + h * a.v_head + (t0 + u) * a.v_row + l * 8) = dequantise8(vc, vs[u]);
   }
-  const uint32_t other = __shfl_xor_sync(0xffffffffu, vw, 4);
-  const uint32_t vc = (q & 1) ? __byte_perm(other, vw, 0x7632) : __byte_perm(vw, other, 0x5410);
-  if (slot < 0) return;
-  *reinterpret_cast<uint4*>(a.K + h * a.k_head + t * a.k_row + l * 8) = dequantise8(kc, ks);
-  *reinterpret_cast<uint4*>(a.V + h * a.v_head + t * a.v_row + l * 8) = dequantise8(vc, vs);
 }
 
 msa_status row_args(const msa_kv4_cache* cache, const void* K, const void* V, const msa_strides* s,
@@ -415,7 +444,8 @@ msa_status row_args(const msa_kv4_cache* cache, const void* K, const void* V, co
 }
 
 unsigned row_blocks(const RowArgs& a) {
-  return (unsigned)((a.T * a.c.Hkv + ROW_THREADS / 16 - 1) / (ROW_THREADS / 16));
+  const int64_t items = (a.T + ROW_UNROLL - 1) / ROW_UNROLL * a.c.Hkv;
+  return (unsigned)((items + ROW_THREADS / 16 - 1) / (ROW_THREADS / 16));
 }
 
 }  // namespace

@@ -6,7 +6,7 @@
 
 namespace msa {
 
-constexpr int KV4_MAX_B = 4096;  // requests of one call: their prefix sums stay in shared memory
+constexpr int KV4_MAX_B = 2048;  // requests of one call: their prefix sums stay in shared memory
 
 struct Kv4View {
   uint8_t* pages;

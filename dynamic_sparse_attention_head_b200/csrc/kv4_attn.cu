@@ -44,6 +44,7 @@ namespace {
 constexpr int HD = 128;       // channels
 constexpr int MAX_CTAS = 160;
 constexpr int MAX_ROWS = 16;  // query rows of a tile, most
+constexpr int MAX_WARP_ROWS = 128;  // warps times rows of a CTA, most
 constexpr int PART = HD + 2;  // floats of a partial row: O, running maximum, sum
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float NEG_INF = -__builtin_huge_valf();
@@ -60,6 +61,7 @@ struct AttendArgs {
   float* lse;
   uint32_t* arrivals;  // [MAX_CTAS]
   float* partial;      // [MAX_CTAS][2][MAX_ROWS][PART]
+  float* heads;        // [MAX_CTAS][warp][rows][HD]: results of segments that began in a warp before
 };
 
 // One (request, KV head, tile of query rows) and its place on the line of key tiles.
@@ -96,15 +98,19 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 
 // Codes in bits 0-3 (4-7) of both halves as fp16 code - 8 (16 (code - 8)): the code is set into the
 // mantissa of 1024, whose step is one, and 1024 + 8 (1024 + 128) is taken off; both are exact.
-__device__ __forceinline__ uint32_t centred_lo(uint32_t w) {
-  const uint32_t v = (w & 0x000f000fu) | 0x64006400u;
-  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), __half2{__ushort_as_half(0x6408), __ushort_as_half(0x6408)});
+template <uint32_t MASK, uint32_t BASE>
+__device__ __forceinline__ uint32_t centred(uint32_t w, uint32_t k1024) {
+  uint32_t v;  // (w & MASK) | k1024 in one instruction
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "n"(MASK), "r"(k1024));
+  const uint32_t b = BASE;
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
-__device__ __forceinline__ uint32_t centred_hi(uint32_t w) {
-  const uint32_t v = (w & 0x00f000f0u) | 0x64006400u;
-  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), __half2{__ushort_as_half(0x6480), __ushort_as_half(0x6480)});
-  return *reinterpret_cast<const uint32_t*>(&d);
+__device__ __forceinline__ uint32_t centred_lo(uint32_t w, uint32_t k1024) {
+  return centred<0x000f000fu, 0x64086408u>(w, k1024);
+}
+__device__ __forceinline__ uint32_t centred_hi(uint32_t w, uint32_t k1024) {
+  return centred<0x00f000f0u, 0x64806480u>(w, k1024);
 }
 
 // 1 / v of a power of two
@@ -145,8 +151,7 @@ struct AttendSmem {
   static constexpr int ROWS = 8 * NT;
   static constexpr int ROW_BYTES = ROWS * HD * 4;
   static constexpr int RING = 0;  // a warp's tail result lies in its ring once its tiles are used up
-  static constexpr int HEADS = W * STAGES * TILE;                // [W][ROWS][HD]
-  static constexpr int STATS = HEADS + W * ROW_BYTES;            // [W][head, tail][ROWS][2]
+  static constexpr int STATS = W * STAGES * TILE;                // [W][head, tail][ROWS][2]
   static constexpr int SEGS = STATS + W * 2 * ROWS * 2 * 4;      // [W + 1]: tails; the CTA's head
   static constexpr int BARS = SEGS + (W + 1) * (int)sizeof(Segment);
   static constexpr int CUM = BARS + W * STAGES * 8;              // [B + 1]
@@ -154,15 +159,15 @@ struct AttendSmem {
   static_assert(BARS % 8 == 0 && CUM % 4 == 0, "alignment");
 };
 
-template <int NG, int NT, int TK, int W, int STAGES>
+template <int NG, int NT, int TK, int CK, int W, int STAGES>
 __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs a) {
   using S = AttendSmem<NG, NT, TK, W, STAGES>;
   using Blk = Kv4Block<NG>;
   constexpr int ROWS = 8 * NT;
-  constexpr int MT = TK / 16;  // operand tiles of 16 keys
+  constexpr int MT = CK / 16;  // operand tiles of 16 keys in one pass
   constexpr int THREADS = W * 32;
   extern __shared__ __align__(128) uint8_t smem[];
-  float* heads = reinterpret_cast<float*>(smem + S::HEADS);
+  float* heads = a.heads + (int64_t)blockIdx.x * W * ROWS * HD;  // [W][ROWS][HD]
   float* stats = reinterpret_cast<float*>(smem + S::STATS);
   Segment* segs = reinterpret_cast<Segment*>(smem + S::SEGS);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BARS);
@@ -297,6 +302,8 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
 
   int c_stage = 0;
   uint32_t c_parity = 0;
+  uint32_t k1024;  // fp16 1024 twice, kept in a register
+  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k1024));
   const int key_of = (g & 1) ? 4 + ((g >> 1) ^ 1) : g >> 1;  // key of operand row g, in 8
   const auto weight = [](float x, float top) { return x == NEG_INF ? 0.f : ex2(x - top); };
   const auto write_row = [&](const Segment& s, int r, int ch, float4 x, float top, float sum) {
@@ -381,7 +388,9 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
       }
     }
 
-    float o[8][NT][4], z[NG][NT][2], m[NT][2], l[NT][2];
+    // base: the running maximum, 0 before there is one (limit is -inf then: any score starts it;
+    // later a score 2^8 above it does)
+    float o[8][NT][4], z[NG][NT][2], base[NT][2], limit[NT][2], l[NT][2];
     float vtop = 0x1p-100f;  // power of two above every V step so far
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -391,16 +400,17 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
         for (int e = 0; e < 4; ++e) o[t][nt][e] = 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m[nt][e] = NEG_INF;
+        base[nt][e] = 0.f;
+        limit[nt][e] = NEG_INF;
         l[nt][e] = 0.f;
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) z[gr][nt][e] = 0.f;
       }
     }
 
-    // One tile.  PARTIAL: some keys are hidden, from all rows (behind the last row's, or on no page)
+    // CK keys of a tile, from its key `in_tile` on.  PARTIAL: some keys are hidden, from all rows (behind the last row's, or on no page)
     // or from some.
-    const auto tile_pass = [&](auto partial_tag, const uint8_t* kb, int tok, uint32_t have) {
+    const auto tile_pass = [&](auto partial_tag, const uint8_t* kb, int tok, int in_tile, uint32_t have) {
       constexpr bool PARTIAL = decltype(partial_tag)::value;
       float sc[MT][NT][4];
       uint32_t vsw[MT][2][NG];
@@ -434,7 +444,7 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int key = tok + 16 * mt + 8 * r + key_of;
-          const bool shown = !PARTIAL || (key < seen && ((have >> ((16 * mt) >> copy_shift)) & 1u));
+          const bool shown = !PARTIAL || (key < seen && ((have >> ((in_tile + 16 * mt) >> copy_shift)) & 1u));
           uint32_t ksw[NG];
           const uint32_t* kp = reinterpret_cast<const uint32_t*>(blk + Blk::K_SCALES + 4 * NG * (key_of + 8 * r));
           const uint32_t* vp = reinterpret_cast<const uint32_t*>(blk + Blk::V_SCALES + 4 * NG * (key_of + 8 * r));
@@ -448,12 +458,10 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float x = 0.f;
+              float x = -base[nt][e];
 #pragma unroll
               for (int gr = 0; gr < NG; ++gr)
-                x = gr == 0 ? fmaf(acc[gr][nt][2 * r + e], bf_lo(ksw[gr]) * to_score, bf_hi(ksw[gr]) * qs[gr][nt][e])
-                            : fmaf(acc[gr][nt][2 * r + e], bf_lo(ksw[gr]) * to_score,
-                                   fmaf(bf_hi(ksw[gr]), qs[gr][nt][e], x));
+                x = fmaf(acc[gr][nt][2 * r + e], bf_lo(ksw[gr]) * to_score, fmaf(bf_hi(ksw[gr]), qs[gr][nt][e], x));
               if (PARTIAL && (!shown || key >= lim[nt][e])) x = NEG_INF;
               sc[mt][nt][2 * r + e] = x;
               top[nt][e] = fmaxf(top[nt][e], x);
@@ -462,7 +470,7 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
       }
       bool grow = vmax > vtop;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) grow |= top[nt][0] > m[nt][0] + 8.f || top[nt][1] > m[nt][1] + 8.f;
+      for (int nt = 0; nt < NT; ++nt) grow |= top[nt][0] > limit[nt][0] || top[nt][1] > limit[nt][1];
       if (__any_sync(0xffffffffu, grow)) {
         // a score 2^8 above the running maximum (or a V step above every one before): the maximum is
         // taken anew and what was summed so far is scaled down
@@ -478,9 +486,15 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
             float x = top[nt][e];
 #pragma unroll
             for (int off = 16; off > 2; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-            const float mn = fmaxf(m[nt][e], x);
-            const float f = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);
-            m[nt][e] = mn;
+            // x: how far the largest score is above `base`, the running maximum (0 where there is none)
+            const bool rises = x > 0.f || (limit[nt][e] == NEG_INF && x > NEG_INF);
+            const float f = rises ? (limit[nt][e] == NEG_INF ? 0.f : ex2(-x)) : 1.f;
+            if (rises) {
+              base[nt][e] += x;
+              limit[nt][e] = 8.f;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) sc[mt][nt][e] -= x, sc[mt][nt][2 + e] -= x;
+            }
             l[nt][e] *= f;
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) z[gr][nt][e] *= f;
@@ -492,11 +506,6 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
           }
       }
       const float vinv = 128.f * inv_pow2(vtop);
-      float base[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) base[nt][e] = m[nt][e] == NEG_INF ? 0.f : m[nt][e];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         uint32_t pf[NG][NT][2];
@@ -507,7 +516,7 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              p[nt][e] = ex2(sc[mt][nt][2 * r + e] - base[nt][e]);
+              p[nt][e] = ex2(sc[mt][nt][2 * r + e]);
               l[nt][e] += p[nt][e];
             }
           const int key = tok + 16 * mt + 8 * r + key_of;
@@ -542,8 +551,8 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
           const uint32_t x = (q >> 1) ? __byte_perm(v[0].y, v[1].y, sel) : __byte_perm(v[0].x, v[1].x, sel);
           const uint32_t y = (q >> 1) ? __byte_perm(v[2].y, v[3].y, sel) : __byte_perm(v[2].x, v[3].x, sel);
           const uint32_t x8 = x >> 8, y8 = y >> 8;
-          const uint32_t a00 = centred_lo(x), a01 = centred_hi(x), a02 = centred_lo(y), a03 = centred_hi(y);
-          const uint32_t a10 = centred_lo(x8), a11 = centred_hi(x8), a12 = centred_lo(y8), a13 = centred_hi(y8);
+          const uint32_t a00 = centred_lo(x, k1024), a01 = centred_hi(x, k1024), a02 = centred_lo(y, k1024), a03 = centred_hi(y, k1024);
+          const uint32_t a10 = centred_lo(x8, k1024), a11 = centred_hi(x8, k1024), a12 = centred_lo(y8, k1024), a13 = centred_hi(y8, k1024);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const uint32_t b0 = pf[q * NG / 4][nt][0], b1 = pf[q * NG / 4][nt][1];
@@ -560,8 +569,12 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
       const uint8_t* kb = ring + c_stage * S::TILE;
       const uint32_t all = (1u << per) - 1, have = there ? (holds >> (4 * c_stage)) & all : 0u;
       const int tok = tile * TK;
-      if (have == all && tok + TK <= seen_first) tile_pass(std::false_type{}, kb, tok, have);
-      else if (have) tile_pass(std::true_type{}, kb, tok, have);
+#pragma unroll 1
+      for (int k = 0; k < TK; k += CK) {
+        const uint8_t* at_k = kb + k / 16 * Blk::BYTES;
+        if (have == all && tok + k + CK <= seen_first) tile_pass(std::false_type{}, at_k, tok + k, k, have);
+        else if (have && tok + k < seen) tile_pass(std::true_type{}, at_k, tok + k, k, have);
+      }
       __syncwarp();  // every lane has read the stage
       --in_flight;
       if (++c_stage == STAGES) c_stage = 0, c_parity ^= 1;
@@ -581,7 +594,7 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
         }
     const float of = vtop * 0.0078125f;  // 1 / 128
     const bool starts = s.first >= w0, stops = s.first + s.count <= w1;
-    // a head (it began in a stretch before) goes to its own place, a tail into the ring, which is
+    // a head (it began in a stretch before) goes to the workspace, a tail into the ring, which is
     // empty then: a tail is a stretch's last segment
     float* mine = starts ? reinterpret_cast<float*>(ring) : heads + warp * ROWS * HD;
     float* mine_st = stats + (2 * warp + (starts ? 1 : 0)) * ROWS * 2;
@@ -590,6 +603,7 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = nt * 8 + 2 * c + e;
+        const float top = limit[nt][e] == NEG_INF ? NEG_INF : base[nt][e];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float zq = z[q * NG / 4][nt][e];
@@ -597,12 +611,12 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
                                        fmaf(o[2 * q + 1][nt][e], of, zq),
                                        fmaf(o[2 * q + 1][nt][2 + e], of * 0.0625f, zq));
           if (starts && stops) {
-            if (r < rows) write_row(s, r, 32 * q + 4 * g, x, m[nt][e], l[nt][e]);
+            if (r < rows) write_row(s, r, 32 * q + 4 * g, x, top, l[nt][e]);
           } else {
             *reinterpret_cast<float4*>(mine + r * HD + 32 * q + 4 * g) = x;
           }
         }
-        if (!(starts && stops) && g == 0) mine_st[2 * r] = m[nt][e], mine_st[2 * r + 1] = l[nt][e];
+        if (!(starts && stops) && g == 0) mine_st[2 * r] = top, mine_st[2 * r + 1] = l[nt][e];
       }
     if (lane == 0) {
       if (!starts) {
@@ -653,7 +667,7 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
       for (int w = max(first, 0); w <= last; ++w) {
         if (!is_in(w)) continue;
         const float* src = w == first ? reinterpret_cast<const float*>(smem + S::RING + w * STAGES * S::TILE) : heads + w * ROWS * HD;
-        const float4 y = *reinterpret_cast<const float4*>(src + r * HD + ch);
+        const float4 y = *reinterpret_cast<const float4*>(src + r * HD + ch);  // heads: written by this CTA
         const float f = weight(member(w)[0], top);
         sum = fmaf(member(w)[1], f, sum);
         x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
@@ -715,32 +729,33 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
   }
 }
 
-template <int NG, int NT, int TK, int W, int STAGES>
+template <int NG, int NT, int TK, int CK, int W, int STAGES>
 cudaError_t launch(const AttendArgs& a, int dev, cudaStream_t st) {
   using S = AttendSmem<NG, NT, TK, W, STAGES>;
-  static_assert(S::CUM + (KV4_MAX_B + 1) * 4 <= 226 * 1024, "shared memory of one CTA");
-  static_assert(8 * NT <= MAX_ROWS, "rows of a partial result");
+  static_assert(S::CUM + (KV4_MAX_B + 1) * 4 <= 226 * 1024 + 512, "shared memory of one CTA");
+  static_assert(8 * NT <= MAX_ROWS && W * 8 * NT <= MAX_WARP_ROWS, "rows of the results in the workspace");
   static std::atomic<uint64_t> ready{0};
   if (device_pending(ready, dev)) {
-    const cudaError_t e = cudaFuncSetAttribute(kv4_attend_kernel<NG, NT, TK, W, STAGES>,
+    const cudaError_t e = cudaFuncSetAttribute(kv4_attend_kernel<NG, NT, TK, CK, W, STAGES>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                S::CUM + (KV4_MAX_B + 1) * 4);
     if (e != cudaSuccess) return e;
     mark_device(ready, dev);
   }
   count_launches(1);
-  kv4_attend_kernel<NG, NT, TK, W, STAGES>
+  kv4_attend_kernel<NG, NT, TK, CK, W, STAGES>
       <<<std::min(sm_count(), MAX_CTAS), W * 32, S::CUM + (a.B + 1) * 4, st>>>(a);
   return cudaGetLastError();
 }
 
 template <int NG>
 cudaError_t launch_rows(const AttendArgs& a, int max_q, int dev, cudaStream_t st) {
-  if ((int64_t)max_q * a.group <= 8) return launch<NG, 1, 64, 8, 2>(a, dev, st);
-  return launch<NG, 2, 32, 8, 3>(a, dev, st);
+  if ((int64_t)max_q * a.group <= 8) return launch<NG, 1, 64, 64, (NG == 4 ? 8 : 12), 2>(a, dev, st);
+  return launch<NG, 2, 32, 32, 8, 3>(a, dev, st);
 }
 
 constexpr size_t ARRIVALS_BYTES = 1024;
+constexpr size_t PARTIAL_BYTES = (size_t)MAX_CTAS * 2 * MAX_ROWS * PART * sizeof(float);
 static_assert(ARRIVALS_BYTES >= MAX_CTAS * 4, "a counter per CTA");
 
 }  // namespace
@@ -751,7 +766,7 @@ using namespace msa;
 extern "C" {
 
 size_t msa_kv4_attend_workspace_bytes(void) {
-  return ARRIVALS_BYTES + (size_t)MAX_CTAS * 2 * MAX_ROWS * PART * sizeof(float);
+  return ARRIVALS_BYTES + PARTIAL_BYTES + (size_t)MAX_CTAS * MAX_WARP_ROWS * HD * sizeof(float);
 }
 
 msa_status msa_kv4_attend(const msa_kv4_cache* cache, const void* Q, void* O, const msa_strides* strides,
@@ -784,6 +799,7 @@ msa_status msa_kv4_attend(const msa_kv4_cache* cache, const void* Q, void* O, co
   a.lse = lse;
   a.arrivals = static_cast<uint32_t*>(ws);
   a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ARRIVALS_BYTES);
+  a.heads = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ARRIVALS_BYTES + PARTIAL_BYTES);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MSA_ERR_CUDA;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);

@@ -24,6 +24,7 @@ namespace {
 
 constexpr int RD = 128;
 constexpr int ROPE_THREADS = 128;
+constexpr int ROPE_BLOCKS = 4;  // per SM
 constexpr int ROPE_GROUPS = ROPE_THREADS / 16;
 
 struct RopeArgs {
@@ -36,7 +37,7 @@ struct RopeArgs {
   int64_t T;
   int32_t Hq, H;  // query heads; all heads
   int32_t run, n_runs;  // heads per 16-lane group, groups per token
-  int32_t dim, interleaved;
+  int32_t dim;
   float eps, scale;
   uint64_t turn[RD / 2];
   uint8_t axis[RD / 2];
@@ -54,7 +55,87 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
   x[4] = bf_lo(v.z), x[5] = bf_hi(v.z), x[6] = bf_lo(v.w), x[7] = bf_hi(v.w);
 }
 
-__global__ void __launch_bounds__(ROPE_THREADS) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+// Two fp32 operations at once (neighbouring channels).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// Walks over the heads h0 .. h1 of one kind (queries or keys) of one token.  With the norm's weights
+// w taken into the cosines, own[e] = w_e cos and other[e] = +-w_partner sin, a row is
+// r * (x * own + x_partner * other), r the row's norm: the partner's channels come over as packed words,
+// before any arithmetic.
+// `ahead`: the first rows, already on their way.
+constexpr int U = 4;
+
+__device__ __forceinline__ void rope_load(uint4 (&v)[U], const __nv_bfloat16* src, int64_t src_head, int left) {
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    v[u] = make_uint4(0, 0, 0, 0);
+    if (u < left) v[u] = __ldcs(reinterpret_cast<const uint4*>(src));
+    src += src_head;
+  }
+}
+
+template <bool NORM, bool INTERLEAVED>
+__device__ __forceinline__ void rope_heads(const __nv_bfloat16* src, int64_t src_head, __nv_bfloat16* dst,
+                                           int64_t dst_head, int heads, bool live, int partner, bool rotated,
+                                           float eps, const float2 (&own)[4], const float2 (&other)[4],
+                                           uint4 (&ahead)[U]) {
+  // the two groups of a warp may have runs of different lengths: the longer one sets the trip count
+  const int trips = __reduce_max_sync(0xffffffffu, (unsigned)((max(heads, 0) + U - 1) / U));
+  for (int k = 0; k < trips; ++k, heads -= U) {
+    uint4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = ahead[u];
+    src += U * src_head;
+    rope_load(ahead, src, src_head, heads - U);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      float2 x[4], y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = make_float2(bf_lo(w[e]), bf_hi(w[e]));
+        // an unrotated channel has no partner: its word is 0, whatever the row holds
+        uint32_t pw = INTERLEAVED ? __funnelshift_l(w[e], w[e], 16) : __shfl_sync(0xffffffffu, w[e], partner);
+        if (!rotated) pw = 0;
+        y[e] = fma2(make_float2(bf_lo(pw), bf_hi(pw)), other[e], mul2(x[e], own[e]));
+      }
+      if (NORM) {
+        float2 s2 = mul2(x[0], x[0]);
+#pragma unroll
+        for (int e = 1; e < 4; ++e) s2 = fma2(x[e], x[e], s2);
+        float ss = s2.x + s2.y;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, 16);
+        const float r = rsqrtf(ss * (1.f / RD) + eps);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], make_float2(r, r));
+      }
+      if (live && u < heads)
+        __stcs(reinterpret_cast<uint4*>(dst),
+               make_uint4(bf_pack(y[0].x, y[0].y), bf_pack(y[1].x, y[1].y), bf_pack(y[2].x, y[2].y),
+                          bf_pack(y[3].x, y[3].y)));
+      dst += dst_head;
+    }
+  }
+}
+
+template <bool INTERLEAVED>
+__global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ uint64_t turn[RD / 2];
   __shared__ uint8_t axis[RD / 2];
   if (threadIdx.x < RD / 2) {
@@ -62,7 +143,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) qk_norm_rope_kernel(const __grid
     axis[threadIdx.x] = a.axis[threadIdx.x];
   }
   __syncthreads();
-  const int l = threadIdx.x & 15;
+  const int l = threadIdx.x & 15, lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * ROPE_GROUPS + (threadIdx.x >> 4);
   // a warp's two groups shuffle together, so a group without a token walks along on the last one
   const bool live = item < a.T * a.n_runs;
@@ -71,84 +152,62 @@ __global__ void __launch_bounds__(ROPE_THREADS) qk_norm_rope_kernel(const __grid
   const int h0 = (int)(it - t * a.n_runs) * a.run;
   const int h1 = min(h0 + a.run, a.H);
   const int lanes = a.dim >> 3, half = lanes >> 1;  // lanes that hold rotated channels
+  const bool rotated = l < lanes;
+  // every lane shuffles; lanes behind the rotated channels read their own value
+  const int partner = INTERLEAVED || !rotated ? lane : (l < half ? lane + half : lane - half);
 
-  float cs[8], sn[8];
+  // the first rows are asked for before the angles are worked out
+  const int k0 = max(h0 - a.Hq, 0), n_q = min(h1, a.Hq) - h0, n_k = h1 - a.Hq - k0;
+  const __nv_bfloat16 *q_src = a.Q + h0 * a.q_head + t * a.q_row + l * 8, *k_src = a.K + k0 * a.k_head + t * a.k_row + l * 8;
+  uint4 q_ahead[U], k_ahead[U];
+  rope_load(q_ahead, q_src, a.q_head, n_q);
+  rope_load(k_ahead, k_src, a.k_head, n_k);
+
+  float cs[8], sn[8];  // of this lane's channels; the sine with the sign of its place in the pair
 #pragma unroll
   for (int e = 0; e < 8; ++e) cs[e] = 1.f, sn[e] = 0.f;
-  if (l < lanes) {
-    const int n = a.interleaved ? 4 : 8;
-    const int i0 = a.interleaved ? 4 * l : 8 * (l < half ? l : l - half);
+  if (rotated) {
+    const int i0 = INTERLEAVED ? 4 * l : 8 * (l < half ? l : l - half);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      if (e >= n) break;
-      const int64_t p = a.pos[axis[i0 + e] * a.pos_stride + t];
-      const uint64_t ph = (uint64_t)p * turn[i0 + e];
+      if (INTERLEAVED && (e & 1)) {
+        cs[e] = cs[e - 1], sn[e] = -sn[e - 1];
+        continue;
+      }
+      const int i = i0 + (INTERLEAVED ? e / 2 : e);
+      const int64_t p = a.pos[axis[i] * a.pos_stride + t];
+      const uint64_t ph = (uint64_t)p * turn[i];
       sincospif((float)(int32_t)(ph >> 32) * 0x1p-31f, &sn[e], &cs[e]);
       cs[e] *= a.scale;
-      sn[e] *= a.scale;
-    }
-    if (!a.interleaved && l < half) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sn[e] = -sn[e];
+      sn[e] *= (INTERLEAVED || l < half) ? -a.scale : a.scale;
     }
   }
-  // every lane shuffles; lanes behind the rotated channels take their own value (sine 0)
-  const int lane = threadIdx.x & 31;
-  const int partner = a.interleaved || l >= lanes ? lane : (l < half ? lane + half : lane - half);
-
-  constexpr int U = 4;
-  // groups of one warp may have runs of different lengths: the longer one sets the trip count
-  const int trips = __reduce_max_sync(0xffffffffu, (unsigned)((h1 - h0 + U - 1) / U));
-  for (int k = 0; k < trips; ++k) {
-    uint4 v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + k * U + u;
-      v[u] = make_uint4(0, 0, 0, 0);
-      if (h < h1)
-        v[u] = *reinterpret_cast<const uint4*>((h < a.Hq ? a.Q + h * a.q_head + t * a.q_row
-                                                         : a.K + (h - a.Hq) * a.k_head + t * a.k_row) + l * 8);
+  for (int kind = 0; kind < 2; ++kind) {
+    const uint4* w = kind ? a.wk : a.wq;
+    float2 own[4], other[4];
+    float g[8], gp[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = gp[e] = 1.f;
+    if (w) {
+      unpack8(__ldg(w + l), g);
+      float q[8];
+      unpack8(__ldg(w + (partner & 15)), q);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) gp[e] = INTERLEAVED ? g[e ^ 1] : q[e];
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + k * U + u;
-      const bool is_q = h < a.Hq;
-      float x[8];
-      unpack8(v[u], x);
-      const uint4* w = is_q ? a.wq : a.wk;
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, 16);
-      if (w) {
-        const float r = rsqrtf(ss * (1.f / RD) + a.eps);
-        float g[8];
-        unpack8(__ldg(w + l), g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * r * g[e];
-      }
-      float y[8];
-      if (a.interleaved) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[2 * e] = l < lanes ? x[2 * e] * cs[e] - x[2 * e + 1] * sn[e] : x[2 * e];
-          y[2 * e + 1] = l < lanes ? x[2 * e + 1] * cs[e] + x[2 * e] * sn[e] : x[2 * e + 1];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float o = __shfl_sync(0xffffffffu, x[e], partner);
-          y[e] = l < lanes ? fmaf(o, sn[e], x[e] * cs[e]) : x[e];
-        }
-      }
-      if (live && h < h1) {
-        __nv_bfloat16* d = (is_q ? a.Qo + h * a.qo_head + t * a.qo_row
-                                 : a.Ko + (h - a.Hq) * a.ko_head + t * a.ko_row) + l * 8;
-        *reinterpret_cast<uint4*>(d) =
-            make_uint4(bf_pack(y[0], y[1]), bf_pack(y[2], y[3]), bf_pack(y[4], y[5]), bf_pack(y[6], y[7]));
-      }
+    for (int e = 0; e < 4; ++e) {
+      own[e] = make_float2(g[2 * e] * cs[2 * e], g[2 * e + 1] * cs[2 * e + 1]);
+      other[e] = make_float2(gp[2 * e] * sn[2 * e], gp[2 * e + 1] * sn[2 * e + 1]);
     }
+    const int n = kind ? n_k : n_q;
+    const __nv_bfloat16* src = kind ? k_src : q_src;
+    __nv_bfloat16* dst = (kind ? a.Ko + k0 * a.ko_head + t * a.ko_row : a.Qo + h0 * a.qo_head + t * a.qo_row) + l * 8;
+    const int64_t sh = kind ? a.k_head : a.q_head, dh = kind ? a.ko_head : a.qo_head;
+    uint4(&ahead)[U] = kind ? k_ahead : q_ahead;
+    if (w) rope_heads<true, INTERLEAVED>(src, sh, dst, dh, n, live, partner, rotated, a.eps, own, other, ahead);
+    else rope_heads<false, INTERLEAVED>(src, sh, dst, dh, n, live, partner, rotated, a.eps, own, other, ahead);
   }
 }
 
@@ -204,7 +263,7 @@ extern "C" msa_status msa_qk_norm_rope(const void* Q, const void* K, const msa_s
   a.wq = static_cast<const uint4*>(wq), a.wk = static_cast<const uint4*>(wk);
   a.pos = positions, a.pos_stride = pos_stride;
   a.T = T, a.Hq = Hq, a.H = Hq + Hkv;
-  a.dim = rope->dim, a.interleaved = rope->interleaved != 0;
+  a.dim = rope->dim;
   a.eps = eps, a.scale = rope->scale;
   // the longest run of heads that still leaves 64 groups for every SM: a run shares its cosines
   a.run = a.H;
@@ -213,6 +272,8 @@ extern "C" msa_status msa_qk_norm_rope(const void* Q, const void* K, const msa_s
   const int64_t blocks = (T * a.n_runs + ROPE_GROUPS - 1) / ROPE_GROUPS;
   if (blocks > 0x7fffffff) return MSA_ERR_UNSUPPORTED;
   count_launches(1);
-  qk_norm_rope_kernel<<<(unsigned)blocks, ROPE_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (rope->interleaved) qk_norm_rope_kernel<true><<<(unsigned)blocks, ROPE_THREADS, 0, cs>>>(a);
+  else qk_norm_rope_kernel<false><<<(unsigned)blocks, ROPE_THREADS, 0, cs>>>(a);
   return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }

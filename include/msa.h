@@ -410,7 +410,7 @@ size_t msa_kv4_page_bytes(int32_t page_tokens, int32_t group);
  * A request that does not fit its row (or has a negative length, whose new tokens then count as
  * none) gets no pages; from the first request on that the free pages do not suffice for, none
  * does: their slots are -1, kv_lens_out = kv_lens, and the error is recorded (msa_kv4_status).
- * B <= 4096.  Every pointer is a device pointer. */
+ * B <= 2048.  Every pointer is a device pointer. */
 msa_status msa_kv4_slots(const msa_kv4_cache* cache, const int32_t* kv_lens, const int32_t* new_lens, int32_t B,
                          int32_t* block_table, int64_t table_stride, int32_t max_blocks, const int32_t* free_pages,
                          const int32_t* n_free, int32_t* kv_lens_out, int32_t* n_free_out, int32_t* cu_new,
@@ -418,7 +418,7 @@ msa_status msa_kv4_slots(const msa_kv4_cache* cache, const int32_t* kv_lens, con
 
 /* Gives back the pages of the requests ids[0 .. n): pushed on the free stack in the order of the
  * list, their kv_lens set to 0 and their table entries to -1.  An id named twice counts once; an id
- * outside [0, B) is recorded as an error.  n <= 4096. */
+ * outside [0, B) is recorded as an error.  n <= 2048. */
 msa_status msa_kv4_release(const msa_kv4_cache* cache, const int32_t* ids, int32_t n, int32_t* kv_lens, int32_t B,
                            int32_t* block_table, int64_t table_stride, int32_t max_blocks, int32_t* free_pages,
                            int32_t* n_free, void* stream);
@@ -444,7 +444,7 @@ msa_status msa_kv4_read(const msa_kv4_cache* cache, void* K, void* V, const msa_
  * head h / (Hq / Hkv).  Any number of query tokens per request (one each: decoding; a few: draft
  * verification; many: a prompt over a cached prefix); max_q, the most of any request, picks the
  * kernel's tile and nothing else.  Page numbers outside the cache hide their keys, lengths outside
- * the table row or Q are cut, and both are recorded as an error.  B <= 4096.
+ * the table row or Q are cut, and both are recorded as an error.  B <= 2048.
  * ws: device, 256-byte aligned, msa_kv4_attend_workspace_bytes() bytes, zero-filled once by the
  * caller; every call leaves it ready for the next, of any shape.  Calls that may overlap on the GPU
  * need a workspace each.  Sums in fp32 and in a fixed order: the same inputs give the same bits. */

@@ -96,8 +96,8 @@ def test_slots_empty_batch_and_empty_requests():
 
 def test_slots_most_requests():
     rng = np.random.default_rng(1)
-    kv = rng.integers(0, 40, 4096).tolist()
-    _slots(kv, rng.integers(0, 4, 4096).tolist(), 16, 4, 16000, 4096, True)
+    kv = rng.integers(0, 40, 2048).tolist()
+    _slots(kv, rng.integers(0, 4, 2048).tolist(), 16, 4, 8000, 2048, True)
 
 
 def test_slots_out_of_pages_and_rows():

@@ -114,13 +114,13 @@ def test_slots_release_argument_checks():
                dict(nfo=None), dict(cu=None), dict(sl=None), dict(pos=None), dict(cap=-1), dict(blocks=-1)):
         assert slots(**kw) == INVALID, kw
     assert slots(stride=7) == SHAPE and slots(sl=FAKE + 4) == ALIGN
-    assert slots(B=4097) == UNSUPPORTED and slots(blocks=1 << 26, stride=1 << 26) == UNSUPPORTED
+    assert slots(B=2049) == UNSUPPORTED and slots(blocks=1 << 26, stride=1 << 26) == UNSUPPORTED
 
     def release(ids=FAKE, n=2, kv=FAKE, B=2, table=FAKE, stride=8, blocks=8, free=FAKE, nf=FAKE):
         return _lib.msa_kv4_release(_cache(), ids, n, kv, B, table, stride, blocks, free, nf, None)
     for kw in (dict(ids=None), dict(n=-1), dict(kv=None), dict(B=-1), dict(table=None), dict(free=None), dict(nf=None)):
         assert release(**kw) == INVALID, kw
-    assert release(stride=7) == SHAPE and release(n=4097) == UNSUPPORTED
+    assert release(stride=7) == SHAPE and release(n=2049) == UNSUPPORTED
     assert release(n=0, ids=None) == 0
 
 
@@ -139,7 +139,7 @@ def test_attend_argument_checks():
     for kw in (dict(Q=FAKE + 8), dict(O=FAKE + 2), dict(w=FAKE + 128), dict(s=_strides(row=4))):
         assert call(**kw) == ALIGN, kw
     assert call(wb=ws - 1) == WORKSPACE
-    assert call(B=4097) == UNSUPPORTED and call(blocks=1 << 26, stride=1 << 26) == UNSUPPORTED
+    assert call(B=2049) == UNSUPPORTED and call(blocks=1 << 26, stride=1 << 26) == UNSUPPORTED
     assert call(T=1 << 30, Hq=16) == UNSUPPORTED
     assert call(T=0, Q=None, O=None) == 0 and call(B=0, kv=None, cu=None, table=None) == 0
 
