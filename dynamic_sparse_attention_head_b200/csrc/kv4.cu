@@ -286,19 +286,21 @@ __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Eight channels of a row (lane l of 16: channels 8 l .. 8 l + 7) to eight codes in channel order,
-// and the group's (step, lo) word.  Smallest and largest value are found together, as the smallest
-// of x and of -x in the two halves of a word; a NaN in either is kept.  The product (x - lo) * r is
-// rounded to a whole number in one step, by adding 1.5 * 2^23 in the same fused operation: a value
-// next to a border falls on its own side, as it would in 64 bits.
+// Sixteen channels of a row (lane l of 8: channels 16 l .. 16 l + 15) to sixteen codes in channel
+// order, and the group's (step, lo) word.  Smallest and largest value are found together, as the
+// smallest of x and of -x in the two halves of a word; a NaN in either is kept.  The product
+// (x - lo) * r is rounded to a whole number in one step, by adding 1.5 * 2^23 in the same fused
+// operation: a value next to a border falls on its own side, as it would in 64 bits.
 template <int NG>
-__device__ __forceinline__ uint32_t quantise8(const uint4& v, uint32_t& scale_word) {
+__device__ __forceinline__ uint2 quantise16(const uint4 (&v)[2], uint32_t& scale_word) {
   constexpr uint32_t SIGNS = 0x80008000u;
-  const uint32_t lo2 = min2_nan(min2_nan(v.x, v.y), min2_nan(v.z, v.w));
-  const uint32_t hi2 = min2_nan(min2_nan(v.x ^ SIGNS, v.y ^ SIGNS), min2_nan(v.z ^ SIGNS, v.w ^ SIGNS));
+  const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+  uint32_t lo2 = w[0], hi2 = w[0] ^ SIGNS;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) lo2 = min2_nan(lo2, w[i]), hi2 = min2_nan(hi2, w[i] ^ SIGNS);
   uint32_t both = min2_nan(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));  // low half lo, high half -hi
 #pragma unroll
-  for (int o = 8 / NG; o > 0; o >>= 1) both = min2_nan(both, __shfl_xor_sync(0xffffffffu, both, o));
+  for (int o = 4 / NG; o > 0; o >>= 1) both = min2_nan(both, __shfl_xor_sync(0xffffffffu, both, o));
   const float lo = bf_lo(both), range = -bf_hi(both) - lo;
   // range / 15, correctly rounded: a product with the rounded reciprocal and one correction by the
   // exact remainder (Markstein, 1990)
@@ -307,33 +309,34 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& v, uint32_t& scale_wo
   float step = __bfloat162float(__float2bfloat16_rn(q));
   if (step < 0x1p-126f) step = 0.f;
   const float r = step > 0.f ? __frcp_rn(step) : 0.f;
-  const float x[8] = {bf_lo(v.x), bf_hi(v.x), bf_lo(v.y), bf_hi(v.y), bf_lo(v.z), bf_hi(v.z), bf_lo(v.w), bf_hi(v.w)};
   // a code is the low bits of the sum (no larger than 15: step is within 2^-9 of range / 15, so the
   // largest product is below 15.06); shifted sums added up hold the codes and a constant
-  uint32_t code = 0u - 0x4b400000u * 0x11111111u;
+  uint2 code = make_uint2(0u - 0x4b400000u * 0x11111111u, 0u - 0x4b400000u * 0x11111111u);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) code += __float_as_uint(fmaf(__fsub_rn(x[e], lo), r, 12582912.f)) << (4 * e);
+  for (int e = 0; e < 8; ++e) {
+    const float x = (e & 1) ? bf_hi(w[e / 2]) : bf_lo(w[e / 2]), y = (e & 1) ? bf_hi(w[4 + e / 2]) : bf_lo(w[4 + e / 2]);
+    code.x += __float_as_uint(fmaf(__fsub_rn(x, lo), r, 12582912.f)) << (4 * e);
+    code.y += __float_as_uint(fmaf(__fsub_rn(y, lo), r, 12582912.f)) << (4 * e);
+  }
   scale_word = (__float_as_uint(step) >> 16) | (__float_as_uint(lo) & 0xffff0000u);
-  if (!(range < __int_as_float(0x7f800000))) scale_word = 0x7fc07fc0u, code = 0;
+  if (!(range < __int_as_float(0x7f800000))) scale_word = 0x7fc07fc0u, code = make_uint2(0, 0);
   return code;
 }
 
-// Sixteen lanes take one (token, KV head) row, 16 bytes of K and of V each, ROW_UNROLL rows of
-// neighbouring tokens in flight.
-constexpr int ROW_UNROLL = 4;
-
-// The rows of a group: one head, ROW_UNROLL neighbouring tokens; a warp's two groups have neighbouring
-// heads.  Their slots, -1 where there is nothing to do.
-__device__ __forceinline__ void row_item(const RowArgs& a, int64_t& t0, int& h, int64_t (&slot)[ROW_UNROLL]) {
-  const int64_t item = (int64_t)blockIdx.x * (ROW_THREADS / 16) + (threadIdx.x >> 4);
-  const int64_t quad = item / a.c.Hkv;
-  h = (int)(item - quad * a.c.Hkv);
-  t0 = quad * ROW_UNROLL;
+// LANES lanes take one (token, KV head) row of K and of V; the rows of a group are one head's, UNROLL
+// neighbouring tokens in flight, neighbouring groups have neighbouring heads.  Their slots, -1 where
+// there is nothing to do.
+template <int LANES, int UNROLL>
+__device__ __forceinline__ void row_item(const RowArgs& a, int64_t& t0, int& h, int64_t (&slot)[UNROLL]) {
+  const int64_t item = (int64_t)blockIdx.x * (ROW_THREADS / LANES) + threadIdx.x / LANES;
+  const int64_t run = item / a.c.Hkv;
+  h = (int)(item - run * a.c.Hkv);
+  t0 = run * UNROLL;
 #pragma unroll
-  for (int u = 0; u < ROW_UNROLL; ++u) {
+  for (int u = 0; u < UNROLL; ++u) {
     slot[u] = t0 + u < a.T ? a.slots[t0 + u] : -1;
     if (slot[u] >= a.c.n_slots()) {
-      if ((threadIdx.x & 15) == 0) atomicOr(a.c.state, DEV_ERR_BOUNDS);
+      if (threadIdx.x % LANES == 0) atomicOr(a.c.state, DEV_ERR_BOUNDS);
       slot[u] = -1;
     }
   }
@@ -345,44 +348,56 @@ __device__ __forceinline__ uint8_t* row_block(const Kv4View& c, int64_t slot, in
          ((slot & (c.page_tokens() - 1)) >> 4) * Kv4Block<NG>::BYTES;
 }
 
-// Bound by HBM: 512 bytes read and 2 (64 + 4 NG) written per row.
+constexpr int APPEND_LANES = 8, APPEND_UNROLL = 2;
+
+// 512 bytes read and 2 (64 + 4 NG) written per row, by 8 lanes of 16 channels: what is worked out once
+// a group (its extremes, the step, the reciprocal) costs as much as two rows' codes.
 template <int NG>
 __global__ void __launch_bounds__(ROW_THREADS) kv4_append_kernel(const RowArgs a) {
   using Blk = Kv4Block<NG>;
-  const int l = threadIdx.x & 15;
-  int64_t t0, slot[ROW_UNROLL];
+  constexpr int U = APPEND_UNROLL;
+  const int l = threadIdx.x % APPEND_LANES;
+  int64_t t0, slot[U];
   int h;
-  row_item(a, t0, h, slot);
-  uint4 kx[ROW_UNROLL], vx[ROW_UNROLL];
+  row_item<APPEND_LANES>(a, t0, h, slot);
+  uint4 kx[U][2], vx[U][2];
 #pragma unroll
-  for (int u = 0; u < ROW_UNROLL; ++u) {
-    kx[u] = vx[u] = make_uint4(0, 0, 0, 0);
-    if (slot[u] >= 0) {
-      kx[u] = *reinterpret_cast<const uint4*>(a.K + h * a.k_head + (t0 + u) * a.k_row + l * 8);
-      vx[u] = *reinterpret_cast<const uint4*>(a.V + h * a.v_head + (t0 + u) * a.v_row + l * 8);
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      kx[u][i] = vx[u][i] = make_uint4(0, 0, 0, 0);
+      if (slot[u] >= 0) {
+        kx[u][i] = *reinterpret_cast<const uint4*>(a.K + h * a.k_head + (t0 + u) * a.k_row + l * 16 + i * 8);
+        vx[u][i] = *reinterpret_cast<const uint4*>(a.V + h * a.v_head + (t0 + u) * a.v_row + l * 16 + i * 8);
+      }
     }
-  }
-  const int q = l >> 2, g = 2 * (l & 3) + (q & 1);
+  const int q = l >> 1, g = 4 * (l & 1) + 2 * (q & 1);
 #pragma unroll
-  for (int u = 0; u < ROW_UNROLL; ++u) {
+  for (int u = 0; u < U; ++u) {
     uint32_t ks, vs;
-    const uint32_t kc = quantise8<NG>(kx[u], ks), vc = quantise8<NG>(vx[u], vs);
-    // V words hold four channels of two neighbouring quarters of the row (lanes l and l ^ 4): each
-    // lane hands over the half that its partner stores
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, vc, 4);
-    const uint32_t vw = (q & 1) ? __byte_perm(other, vc, 0x7632) : __byte_perm(vc, other, 0x5410);
+    const uint2 kc = quantise16<NG>(kx[u], ks), vc = quantise16<NG>(vx[u], vs);
+    // V words hold four channels of two neighbouring quarters of the row (lanes l and l ^ 2): of its
+    // four fours a lane keeps two and hands over the two that its partner stores
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, (q & 1) ? vc.x : vc.y, 2);
+    const uint32_t even = (q & 1) ? other : vc.x, odd = (q & 1) ? vc.y : other;
     if (slot[u] < 0) continue;
     const int i = (int)(slot[u] & 15);
     uint8_t* blk = row_block<NG>(a.c, slot[u], h);
-    *reinterpret_cast<uint32_t*>(blk + 64 * i + 16 * (l & 3) + 4 * (l >> 2)) = kc;
-    *reinterpret_cast<uint32_t*>(blk + Blk::V_CODES + 64 * i + 8 * (g ^ kv4_v_swizzle(i)) + 4 * (q >> 1)) = vw;
-    if (l % (16 / NG) == 0) {
-      const int grp = l / (16 / NG);
+    uint8_t* kp = blk + 64 * i + 32 * (l & 1) + 4 * q;
+    *reinterpret_cast<uint32_t*>(kp) = kc.x;
+    *reinterpret_cast<uint32_t*>(kp + 16) = kc.y;
+    uint8_t* vp = blk + Blk::V_CODES + 64 * i + 4 * (q >> 1);
+    *reinterpret_cast<uint32_t*>(vp + 8 * (g ^ kv4_v_swizzle(i))) = __byte_perm(even, odd, 0x5410);
+    *reinterpret_cast<uint32_t*>(vp + 8 * ((g + 1) ^ kv4_v_swizzle(i))) = __byte_perm(even, odd, 0x7632);
+    if (l % (APPEND_LANES / NG) == 0) {
+      const int grp = l / (APPEND_LANES / NG);
       *reinterpret_cast<uint32_t*>(blk + Blk::K_SCALES + 4 * NG * i + 4 * grp) = ks;
       *reinterpret_cast<uint32_t*>(blk + Blk::V_SCALES + 4 * NG * i + 4 * grp) = vs;
     }
   }
 }
+
+constexpr int READ_LANES = 16, READ_UNROLL = 4;
 
 __device__ __forceinline__ uint4 dequantise8(uint32_t code, uint32_t scale_word) {
   const float step = bf_lo(scale_word), lo = bf_hi(scale_word);
@@ -397,14 +412,15 @@ __device__ __forceinline__ uint4 dequantise8(uint32_t code, uint32_t scale_word)
 template <int NG>
 __global__ void __launch_bounds__(ROW_THREADS) kv4_read_kernel(const RowArgs a) {
   using Blk = Kv4Block<NG>;
-  const int l = threadIdx.x & 15;
-  int64_t t0, slot[ROW_UNROLL];
+  constexpr int U = READ_UNROLL;
+  const int l = threadIdx.x % READ_LANES;
+  int64_t t0, slot[U];
   int h;
-  row_item(a, t0, h, slot);
+  row_item<READ_LANES>(a, t0, h, slot);
   const int q = l >> 2, g = 2 * (l & 3) + (q & 1), grp = l / (16 / NG);
-  uint32_t kc[ROW_UNROLL], vw[ROW_UNROLL], ks[ROW_UNROLL], vs[ROW_UNROLL];
+  uint32_t kc[U], vw[U], ks[U], vs[U];
 #pragma unroll
-  for (int u = 0; u < ROW_UNROLL; ++u) {
+  for (int u = 0; u < U; ++u) {
     kc[u] = vw[u] = ks[u] = vs[u] = 0;
     if (slot[u] < 0) continue;
     const int i = (int)(slot[u] & 15);
@@ -415,7 +431,7 @@ __global__ void __launch_bounds__(ROW_THREADS) kv4_read_kernel(const RowArgs a) 
     vs[u] = *reinterpret_cast<const uint32_t*>(blk + Blk::V_SCALES + 4 * NG * i + 4 * grp);
   }
 #pragma unroll
-  for (int u = 0; u < ROW_UNROLL; ++u) {
+  for (int u = 0; u < U; ++u) {
     const uint32_t other = __shfl_xor_sync(0xffffffffu, vw[u], 4);
     const uint32_t vc = (q & 1) ? __byte_perm(other, vw[u], 0x7632) : __byte_perm(vw[u], other, 0x5410);
     if (slot[u] < 0) continue;
@@ -443,9 +459,9 @@ msa_status row_args(const msa_kv4_cache* cache, const void* K, const void* V, co
   return MSA_OK;
 }
 
-unsigned row_blocks(const RowArgs& a) {
-  const int64_t items = (a.T + ROW_UNROLL - 1) / ROW_UNROLL * a.c.Hkv;
-  return (unsigned)((items + ROW_THREADS / 16 - 1) / (ROW_THREADS / 16));
+unsigned row_blocks(const RowArgs& a, int lanes, int unroll) {
+  const int64_t items = (a.T + unroll - 1) / unroll * a.c.Hkv;
+  return (unsigned)((items * lanes + ROW_THREADS - 1) / ROW_THREADS);
 }
 
 }  // namespace
@@ -523,11 +539,12 @@ msa_status msa_kv4_append(const msa_kv4_cache* cache, const void* K, const void*
   const msa_status st = row_args(cache, K, V, strides, slots, T, &a);
   if (st != MSA_OK || T == 0) return st;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const unsigned blocks = row_blocks(a, APPEND_LANES, APPEND_UNROLL);
   count_launches(1);
   switch (cache->group) {
-    case 128: kv4_append_kernel<1><<<row_blocks(a), ROW_THREADS, 0, cs>>>(a); break;
-    case 64: kv4_append_kernel<2><<<row_blocks(a), ROW_THREADS, 0, cs>>>(a); break;
-    default: kv4_append_kernel<4><<<row_blocks(a), ROW_THREADS, 0, cs>>>(a); break;
+    case 128: kv4_append_kernel<1><<<blocks, ROW_THREADS, 0, cs>>>(a); break;
+    case 64: kv4_append_kernel<2><<<blocks, ROW_THREADS, 0, cs>>>(a); break;
+    default: kv4_append_kernel<4><<<blocks, ROW_THREADS, 0, cs>>>(a); break;
   }
   return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
@@ -538,11 +555,12 @@ msa_status msa_kv4_read(const msa_kv4_cache* cache, void* K, void* V, const msa_
   const msa_status st = row_args(cache, K, V, strides, slots, T, &a);
   if (st != MSA_OK || T == 0) return st;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const unsigned blocks = row_blocks(a, READ_LANES, READ_UNROLL);
   count_launches(1);
   switch (cache->group) {
-    case 128: kv4_read_kernel<1><<<row_blocks(a), ROW_THREADS, 0, cs>>>(a); break;
-    case 64: kv4_read_kernel<2><<<row_blocks(a), ROW_THREADS, 0, cs>>>(a); break;
-    default: kv4_read_kernel<4><<<row_blocks(a), ROW_THREADS, 0, cs>>>(a); break;
+    case 128: kv4_read_kernel<1><<<blocks, ROW_THREADS, 0, cs>>>(a); break;
+    case 64: kv4_read_kernel<2><<<blocks, ROW_THREADS, 0, cs>>>(a); break;
+    default: kv4_read_kernel<4><<<blocks, ROW_THREADS, 0, cs>>>(a); break;
   }
   return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }
