@@ -1,5 +1,7 @@
 // The paged 4-bit cache's format (msa_kv4_cache) as the kernels address it.
 #pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "msa_internal.h"
@@ -29,6 +31,48 @@ struct Kv4Block {  // 16 tokens of one KV head
 };
 
 __host__ __device__ __forceinline__ constexpr int kv4_v_swizzle(int i) { return 4 * ((i >> 1) & 1); }
+
+constexpr int KV4_MAX_CTAS = 160;  // of an attention launch
+
+struct AttendArgs {
+  Kv4View c;
+  const __nv_bfloat16* Q;
+  __nv_bfloat16* O;
+  int64_t q_head, q_row, o_head, o_row;
+  const int32_t *table, *kv_lens, *cu_q;
+  int64_t table_stride;
+  int32_t max_blocks, B, total_q, Hq, group;  // group: query heads of a KV head
+  float scale2;                               // softmax scale * log2(e)
+  float* lse;
+  uint32_t* arrivals;  // [KV4_MAX_CTAS]
+  float* partial;      // results of segments over several CTAs
+  float* heads;        // [KV4_MAX_CTAS][warp][rows][128]: results of segments that began in a warp before
+};
+
+// A request's first query row, new tokens and cached tokens, cut to what Q and the table row hold;
+// false: something was cut.
+__device__ __forceinline__ bool request_lens(const AttendArgs& a, int b, int32_t& q0, int32_t& n, int32_t& kv) {
+  bool ok = true;
+  q0 = a.cu_q[b];
+  const int32_t q1 = a.cu_q[b + 1];
+  if (q0 < 0 || q1 < q0 || q1 > a.total_q) {
+    ok = false;
+    n = 0;
+  } else {
+    n = q1 - q0;
+  }
+  kv = a.kv_lens[b];
+  const int64_t most = (int64_t)a.max_blocks << a.c.page_shift;
+  if (kv < 0 || kv > most) {
+    ok = false;
+    kv = kv < 0 ? 0 : (int32_t)most;
+  }
+  return ok;
+}
+
+// Many query rows (kv4_prompt.cu): two launches; `partial` holds kv4_prompt_partial_bytes().
+size_t kv4_prompt_partial_bytes();
+cudaError_t launch_kv4_prompt(const AttendArgs& a, int ng, int dev, cudaStream_t st);
 
 // Argument checks shared by the calls, and the view the kernels get.
 msa_status kv4_view(const msa_kv4_cache* c, Kv4View* v);

@@ -42,27 +42,11 @@ namespace msa {
 namespace {
 
 constexpr int HD = 128;       // channels
-constexpr int MAX_CTAS = 160;
 constexpr int MAX_ROWS = 16;  // query rows of a tile, most
 constexpr int MAX_WARP_ROWS = 128;  // warps times rows of a CTA, most
 constexpr int PART = HD + 2;  // floats of a partial row: O, running maximum, sum
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float NEG_INF = -__builtin_huge_valf();
-
-struct AttendArgs {
-  Kv4View c;
-  const __nv_bfloat16* Q;
-  __nv_bfloat16* O;
-  int64_t q_head, q_row, o_head, o_row;
-  const int32_t *table, *kv_lens, *cu_q;
-  int64_t table_stride;
-  int32_t max_blocks, B, total_q, Hq, group;  // group: query heads of a KV head
-  float scale2;                               // softmax scale * log2(e)
-  float* lse;
-  uint32_t* arrivals;  // [MAX_CTAS]
-  float* partial;      // [MAX_CTAS][2][MAX_ROWS][PART]
-  float* heads;        // [MAX_CTAS][warp][rows][HD]: results of segments that began in a warp before
-};
 
 // One (request, KV head, tile of query rows) and its place on the line of key tiles.
 struct Segment {
@@ -123,26 +107,6 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 template <int NT>
 __device__ __forceinline__ int row_tiles(int32_t n, int32_t group) {
   return (int)(((int64_t)n * group + 8 * NT - 1) / (8 * NT));
-}
-
-// The request's new tokens and cached tokens, cut to what Q and the table row hold.
-__device__ __forceinline__ bool request_lens(const AttendArgs& a, int b, int32_t& q0, int32_t& n, int32_t& kv) {
-  bool ok = true;
-  q0 = a.cu_q[b];
-  const int32_t q1 = a.cu_q[b + 1];
-  if (q0 < 0 || q1 < q0 || q1 > a.total_q) {
-    ok = false;
-    n = 0;
-  } else {
-    n = q1 - q0;
-  }
-  kv = a.kv_lens[b];
-  const int64_t most = (int64_t)a.max_blocks << a.c.page_shift;
-  if (kv < 0 || kv > most) {
-    ok = false;
-    kv = kv < 0 ? 0 : (int32_t)most;
-  }
-  return ok;
 }
 
 template <int NG, int NT, int TK, int W, int STAGES>
@@ -744,7 +708,7 @@ cudaError_t launch(const AttendArgs& a, int dev, cudaStream_t st) {
   }
   count_launches(1);
   kv4_attend_kernel<NG, NT, TK, CK, W, STAGES>
-      <<<std::min(sm_count(), MAX_CTAS), W * 32, S::CUM + (a.B + 1) * 4, st>>>(a);
+      <<<std::min(sm_count(), KV4_MAX_CTAS), W * 32, S::CUM + (a.B + 1) * 4, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -754,9 +718,10 @@ cudaError_t launch_rows(const AttendArgs& a, int max_q, int dev, cudaStream_t st
   return launch<NG, 2, 32, 32, 8, 3>(a, dev, st);
 }
 
+constexpr int PROMPT_ROWS = 64;  // query rows of a KV head from which on the tensor-memory kernel is taken
 constexpr size_t ARRIVALS_BYTES = 1024;
-constexpr size_t PARTIAL_BYTES = (size_t)MAX_CTAS * 2 * MAX_ROWS * PART * sizeof(float);
-static_assert(ARRIVALS_BYTES >= MAX_CTAS * 4, "a counter per CTA");
+constexpr size_t PARTIAL_BYTES = (size_t)KV4_MAX_CTAS * 2 * MAX_ROWS * PART * sizeof(float);
+static_assert(ARRIVALS_BYTES >= KV4_MAX_CTAS * 4, "a counter per CTA");
 
 }  // namespace
 }  // namespace msa
@@ -766,7 +731,8 @@ using namespace msa;
 extern "C" {
 
 size_t msa_kv4_attend_workspace_bytes(void) {
-  return ARRIVALS_BYTES + PARTIAL_BYTES + (size_t)MAX_CTAS * MAX_WARP_ROWS * HD * sizeof(float);
+  return ARRIVALS_BYTES + std::max(PARTIAL_BYTES + (size_t)KV4_MAX_CTAS * MAX_WARP_ROWS * HD * sizeof(float),
+                                   kv4_prompt_partial_bytes());
 }
 
 msa_status msa_kv4_attend(const msa_kv4_cache* cache, const void* Q, void* O, const msa_strides* strides,
@@ -804,7 +770,8 @@ msa_status msa_kv4_attend(const msa_kv4_cache* cache, const void* Q, void* O, co
   if (cudaGetDevice(&dev) != cudaSuccess) return MSA_ERR_CUDA;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  switch (cache->group) {
+  if ((int64_t)max_q * a.group >= PROMPT_ROWS) e = launch_kv4_prompt(a, 128 / cache->group, dev, cs);
+  else switch (cache->group) {
     case 128: e = launch_rows<1>(a, max_q, dev, cs); break;
     case 64: e = launch_rows<2>(a, max_q, dev, cs); break;
     default: e = launch_rows<4>(a, max_q, dev, cs); break;

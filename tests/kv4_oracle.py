@@ -128,9 +128,10 @@ def parts(pages, page, group, slot, h):
 
 
 # ---- attention -----------------------------------------------------------------------------------
-def attend(pages, page, group, Q, table, kv_lens, cu_q, scale, hidden=lambda b, j: False):
+def attend(pages, page, group, Q, table, kv_lens, cu_q, scale, hidden=lambda b, j: False, wide=False):
     """Q [Hq, T, 128] -> O, lse and the error bound of each element (see `tolerance`), float64; rows behind
-    cu_q[-1] are NaN in all three.  hidden(b, j): keys on no page."""
+    cu_q[-1] are NaN in all three.  hidden(b, j): keys on no page; wide: the bound of the kernel for
+    many query rows."""
     Hq, T, _ = Q.shape
     Hkv = pages.shape[1]
     G = Hq // Hkv
@@ -144,10 +145,11 @@ def attend(pages, page, group, Q, table, kv_lens, cu_q, scale, hidden=lambda b, 
             ps = [parts(pages, page, group, int(table[b, j // page]) * page + j % page, h)
                   if not hidden(b, j) else [(np.zeros(D, int), np.zeros(D), np.zeros(D))] * 2 for j in range(kv)]
             shown = np.array([not hidden(b, j) for j in range(kv)], bool)
-            K, V, Ka, Va, St = np.zeros((kv, D)), np.zeros((kv, D)), np.zeros((kv, D)), np.zeros((kv, D)), 0.0
+            K, V, Ka, Va, St, Ks = np.zeros((kv, D)), np.zeros((kv, D)), np.zeros((kv, D)), np.zeros((kv, D)), 0.0, 0.0
             for j, ((kc, ks, kl), (vc, vs, vl)) in enumerate(ps):
                 K[j], V[j] = kl + kc * ks, vl + vc * vs
                 Ka[j], Va[j] = np.abs(kl) + kc * ks, np.abs(vl + 8 * vs) + 8 * vs
+                Ks = max(Ks, float(np.nanmax(ks)) if not np.isnan(ks).all() else 0.0)
                 St = max(St, float(np.nanmax(vs)) if not np.isnan(vs).all() else 0.0)
             for g in range(G):
                 for i in range(n):
@@ -164,6 +166,9 @@ def attend(pages, page, group, Q, table, kv_lens, cu_q, scale, hidden=lambda b, 
                     O[at], L[at] = p @ V[see] / l, m + np.log(l)
                     tolO[at], tolL[at] = tolerance(O[at], L[at], p / l, Va[see], (Ka[see] @ np.abs(q)).max() * scale,
                                                    int(see.sum()), St)
+                    if wide:
+                        tolO[at], tolL[at] = tolerance_wide(O[at], L[at], p / l, V[see], Va[see], (Ka[see] @ np.abs(q)).max() * scale,
+                                                            int(see.sum()), np.nanmax(np.abs(V)), Ks * np.abs(q).sum() * scale)
     return O, L, tolO, tolL
 
 
@@ -180,4 +185,16 @@ def tolerance(O, lse, p, Va, reach, n, step):
     ds = reach * 2.0 ** -16 + 2.0 ** -21 + (n / 8 + 32) * 2.0 ** -24
     A = p @ Va
     return np.abs(O) * 2.0 ** -8 + A * (2.0 ** -11 + 2 * ds) + n * 15 * step * 2.0 ** -32 + 2.0 ** -130, \
+        ds + 2.0 ** -21 * max(1.0, abs(lse))
+
+
+def tolerance_wide(O, lse, p, V, Va, reach, n, v_max, step_reach):
+    """The same for the kernel that takes many rows.  Scores: exact products, 17 sums of 16 in fp32, a
+    step of the tensor core's within 2^-22 (reach * 17 * 2^-22 < reach * 2^-17), and fp16's subnormals
+    below the tile's largest step: 2^-16 of it per channel (step_reach: largest step times sum |q|).
+    Values are rounded to fp16, 2^-11 relative and 2^-18 of the tile's largest value; probabilities
+    2^-11 relative and 2^-25 each.  Sums over n in fp32: n / 2 * 2^-24 (two running sums)."""
+    ds = (reach + step_reach) * 2.0 ** -16 + 2.0 ** -21 + (n / 2 + 32) * 2.0 ** -24
+    A = p @ np.abs(V)
+    return np.abs(O) * 2.0 ** -8 + A * (2.0 ** -10 + 2 * ds) + v_max * (2.0 ** -18 + n * 2.0 ** -25) + 2.0 ** -130, \
         ds + 2.0 ** -21 * max(1.0, abs(lse))
