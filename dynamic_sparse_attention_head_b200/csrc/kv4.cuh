@@ -32,6 +32,7 @@ struct Kv4Block {  // 16 tokens of one KV head
 
 __host__ __device__ __forceinline__ constexpr int kv4_v_swizzle(int i) { return 4 * ((i >> 1) & 1); }
 
+constexpr int KV4_PROMPT_MAX_B = 1024;
 constexpr int KV4_MAX_CTAS = 160;  // of an attention launch
 
 struct AttendArgs {
@@ -70,7 +71,7 @@ __device__ __forceinline__ bool request_lens(const AttendArgs& a, int b, int32_t
   return ok;
 }
 
-// Many query rows (kv4_prompt.cu): two launches; `partial` holds kv4_prompt_partial_bytes().
+// Many query rows (kv4_prompt.cu), at most KV4_PROMPT_MAX_B requests: two launches; `partial` holds kv4_prompt_partial_bytes().
 size_t kv4_prompt_partial_bytes();
 cudaError_t launch_kv4_prompt(const AttendArgs& a, int ng, int dev, cudaStream_t st);
 

@@ -770,7 +770,7 @@ msa_status msa_kv4_attend(const msa_kv4_cache* cache, const void* Q, void* O, co
   if (cudaGetDevice(&dev) != cudaSuccess) return MSA_ERR_CUDA;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if ((int64_t)max_q * a.group >= PROMPT_ROWS) e = launch_kv4_prompt(a, 128 / cache->group, dev, cs);
+  if ((int64_t)max_q * a.group >= PROMPT_ROWS && B <= KV4_PROMPT_MAX_B) e = launch_kv4_prompt(a, 128 / cache->group, dev, cs);
   else switch (cache->group) {
     case 128: e = launch_rows<1>(a, max_q, dev, cs); break;
     case 64: e = launch_rows<2>(a, max_q, dev, cs); break;

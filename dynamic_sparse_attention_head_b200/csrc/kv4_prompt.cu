@@ -8,15 +8,12 @@
 // warpgroups hold a query row per thread: maximum, exponentials and sums in fp32, O rescaled only
 // when the maximum grows by 2^8 or the values' power of two grows.
 //
-// Scores keep fp32's precision.  A step has 8 bits and a code 4, one more than fp16 holds in a
-// product, so a step is split into its upper 7 bits and its last one, and
-//   q . k = sum_x q_x (code_x stepA) + sum_x q_x (code_x stepB) + sum_g lo_g sum(q_g)
-// is three contractions into one accumulator, every operand exact: two over the 128 channels, and one
-// over 16 columns that hold the groups' lo against sum(q_g) in three fp16 parts.  A power of two is
-// taken out of each tile's keys and each query row, so that fp16's range holds them.  Against keys
-// rounded to fp16 this costs one product more of three; a score was off by 3e-4 with them, 30 times what
-// lse may lose.  Values are lo + code * step in fp16 (11 bits, a power of two taken out of the tile): O
-// is rounded to 8 bits.
+// Scores keep fp32's precision: the operands are exact.  A code less 8 has 3 bits (or is 8, a power of
+// two) and a step has 8, so (code - 8) * step fits fp16's 11 bits; what is left, lo + 8 step per group,
+// meets the group's sum of the query in 16 more columns, each of the two as a sum of two fp16 parts
+// (three of their four products).  A power of two is taken out of each tile's keys and each query row,
+// so that fp16's range holds them.  (Keys rounded to fp16 put a score off by 3e-4, 30 times what lse
+// may lose.)  Values are lo + code * step rounded to fp16's 11 bits: O is rounded to 8.
 //
 // Work: the 256-row pairs of a request see more and more keys; pair f and pair (last - f) together see
 // nearly the same number, so a request's units (tiles, and one more per pair for its start and end)
@@ -24,7 +21,7 @@
 // border leaves fp32 rows in the workspace; a second small kernel joins them in a fixed order.
 //
 // Bound by the softmax warps' instruction issue, as the layer's own attention kernel; the tensor
-// pipe needs 3200 cycles per pair of tiles.
+// pipe needs 2176 cycles per pair of tiles.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -55,6 +52,7 @@ constexpr uint32_t TM_STREAM = 256, TM_OOFF = 128;  // tensor-memory columns: S 
 constexpr int REG_CTRL = 48, REG_SOFTMAX = 200, REG_DEQ = 64;
 static_assert(REG_CTRL + 2 * REG_SOFTMAX + REG_DEQ <= 512, "register split exceeds the launch allocation");
 constexpr int NAN_RING = 4;
+constexpr int DEQ_UNROLL = 2;
 
 struct PairSeg {
   int32_t b, h, rt;      // request, KV head, pair of row tiles
@@ -67,20 +65,20 @@ template <int NG>
 struct PromptSmem {
   static constexpr int TILE = TK / 16 * Kv4Block<NG>::BYTES;
   static constexpr int Q = 0;                             // [2 streams] channels, sums
-  static constexpr int K = Q + 2 * Q_BYTES;               // codes by stepA, by stepB, lo
-  static constexpr int V = K + 2 * OPERAND + EXTRA;
+  static constexpr int K = Q + 2 * Q_BYTES;               // [2 slots] channels, lo + 8 step
+  static constexpr int V = K + 2 * Q_BYTES;
   static constexpr int RAW = V + OPERAND;                 // [2 slots]
-  static constexpr int CONST = RAW + 2 * TILE;            // [K, V][128 keys][NG] half2 (steps; step, lo)
-  static constexpr int CTRL = CONST + 2 * TK * NG * 4;
+  static constexpr int CONST = RAW + 2 * TILE;            // [K, V, V][128 keys][NG] half2 (step, -8 step; step, lo)
+  static constexpr int CTRL = CONST + 3 * TK * NG * 4;
   struct Ctrl {
-    uint64_t raw_full[2], raw_empty[2], scale_full[2], k_full, k_empty, v_full, v_empty;
+    uint64_t raw_full[2], raw_empty[2], scale_full[4], k_full[2], k_empty[2], v_full, v_empty;
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_free[2], drain[2];
     int64_t sums[THREADS / 32];
     int32_t nan_from[NAN_RING][4];  // per segment: first key whose value group is NaN
     uint32_t raw_have[2];           // copies made
-    uint32_t have[2];               // blocks of 16 keys of a tile that hold keys
-    float k_scale[2];               // power of two taken out of the tile's keys
-    int32_t v_exp[2];               // exponent taken out of the values
+    uint32_t have[4];               // blocks of 16 keys of a tile that hold keys
+    float k_scale[4];               // power of two taken out of the tile's keys
+    int32_t v_exp[4];               // exponent taken out of the values
     int32_t warp_exp[2][4];
     uint32_t tmem;
     int32_t abort, bad, lock;
@@ -246,6 +244,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       mbar_init(&ct.raw_full[i], 1);
       mbar_init(&ct.raw_empty[i], 128);
       mbar_init(&ct.scale_full[i], 1);
+      mbar_init(&ct.scale_full[2 + i], 1);
+      mbar_init(&ct.k_full[i], 128);
+      mbar_init(&ct.k_empty[i], 2);
       mbar_init(&ct.q_full[i], 128);
       mbar_init(&ct.s_full[i], 1);
       mbar_init(&ct.p_full[i], 128);
@@ -253,8 +254,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       mbar_init(&ct.o_free[i], 128);
       mbar_init(&ct.drain[i], 1);
     }
-    mbar_init(&ct.k_full, 128);
-    mbar_init(&ct.k_empty, 2);
     mbar_init(&ct.v_full, 128);
     mbar_init(&ct.v_empty, 2);
     fence_barrier_init();
@@ -338,19 +337,18 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       const uint32_t s_col = tmem + TM_STREAM * st;
       uint32_t kt = 0, mine = 0, done = 0;  // tiles of the CTA, tiles and segments of the stream
       bool ok = true;
-      const auto qk = [&] {
+      const auto qk = [&](uint32_t k) {
         tc_fence_after();
-        uint32_t q_addr = smem_addr(smem + S::Q + st * Q_BYTES), k_addr = smem_addr(smem + S::K);
+        uint32_t q_addr = smem_addr(smem + S::Q + st * Q_BYTES), k_addr = smem_addr(smem + S::K + (k & 1) * Q_BYTES);
         asm volatile("" : "+r"(q_addr), "+r"(k_addr));
-        umma_ss(s_col, smem_desc_sw32(q_addr + OPERAND), smem_desc_sw32(k_addr + 2 * OPERAND), IDESC_QK, 0u);
+        umma_ss(s_col, smem_desc_sw32(q_addr + OPERAND), smem_desc_sw32(k_addr + OPERAND), IDESC_QK, 0u);
 #pragma unroll
-        for (int kk = 0; kk < 16; ++kk) {  // stepA, then stepB, against the same queries
-          const uint32_t off = ((kk >> 2) & 1) * ATOM + (kk & 3) * 32, part = (kk >> 3) * OPERAND;
-          umma_ss(s_col, smem_desc_sw128(q_addr + off, 16, 1024), smem_desc_sw128(k_addr + part + off, 16, 1024),
-                  IDESC_QK, 1u);
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * ATOM + (kk & 3) * 32;
+          umma_ss(s_col, smem_desc_sw128(q_addr + off, 16, 1024), smem_desc_sw128(k_addr + off, 16, 1024), IDESC_QK, 1u);
         }
         umma_commit(&ct.s_full[st]);
-        umma_commit(&ct.k_empty);
+        umma_commit(&ct.k_empty[k & 1]);
       };
       for (int at = t0; at < t1 && ok;) {
         const PairSeg s = locate(a, cum, at);
@@ -359,21 +357,22 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
         if (n <= 0) continue;
         if (rows_of(s, st) <= 0) {  // the pair has no rows for this stream: only hand the tiles on
           for (int j = 0; j < n && ok; ++j, ++kt) {
-            ok = mbar_wait(&ct.k_full, kt & 1, abort);
-            if (ok) mbar_arrive(&ct.k_empty);
+            ok = mbar_wait(&ct.k_full[kt & 1], (kt >> 1) & 1, abort);
+            if (ok) mbar_arrive(&ct.k_empty[kt & 1]);
             ok = ok && mbar_wait(&ct.v_full, kt & 1, abort);
             if (ok) mbar_arrive(&ct.v_empty);
           }
           continue;
         }
-        ok = mbar_wait(&ct.q_full[st], done & 1, abort) && mbar_wait(&ct.k_full, kt & 1, abort) && take_lock(&ct.lock, abort);
+        ok = mbar_wait(&ct.q_full[st], done & 1, abort) && mbar_wait(&ct.k_full[kt & 1], (kt >> 1) & 1, abort) &&
+             take_lock(&ct.lock, abort);
         if (!ok) break;
-        qk();
+        qk(kt);
         atomicExch(&ct.lock, 0);
         for (int j = 0; j < n; ++j, ++kt, ++mine) {
           ok = (j > 0 || done == 0 || mbar_wait(&ct.o_free[st], (done - 1) & 1, abort)) &&
                mbar_wait(&ct.v_full, kt & 1, abort) && mbar_wait(&ct.p_full[st], mine & 1, abort) &&
-               (j + 1 == n || mbar_wait(&ct.k_full, (kt + 1) & 1, abort)) &&
+               (j + 1 == n || mbar_wait(&ct.k_full[(kt + 1) & 1], ((kt + 1) >> 1) & 1, abort)) &&
                take_lock(&ct.lock, abort);
           if (!ok) break;
           tc_fence_after();
@@ -384,7 +383,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
             umma_ts(s_col + TM_OOFF, s_col + 8 * kk, smem_desc_sw128(v_addr + kk * 2048, ATOM, 1024), IDESC_PV,
                     (j > 0 || kk > 0) ? 1u : 0u);
           umma_commit(&ct.v_empty);
-          if (j + 1 < n) qk();
+          if (j + 1 < n) qk(kt + 1);
           atomicExch(&ct.lock, 0);
         }
         if (!ok) break;
@@ -448,18 +447,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
             qs[i * NG / 16] += norm * (((bf_lo(v.x) + bf_hi(v.x)) + (bf_lo(v.y) + bf_hi(v.y))) +
                                        ((bf_lo(v.z) + bf_hi(v.z)) + (bf_lo(v.w) + bf_hi(v.w))));
           }
-          // the groups' sums in three parts of 11 bits, columns 3 g, 3 g + 1, 3 g + 2
+          // the groups' sums in two parts of 11 bits: columns 3 g (first), 3 g + 1 (second), 3 g + 2 (first)
           float col[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) col[e] = 0.f;
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) {
-            float left = qs[gr];
-#pragma unroll
-            for (int e = 0; e < 3; ++e) {
-              col[3 * gr + e] = __half2float(__float2half_rn(left));
-              left -= col[3 * gr + e];
-            }
+            col[3 * gr] = col[3 * gr + 2] = __half2float(__float2half_rn(qs[gr]));
+            col[3 * gr + 1] = qs[gr] - col[3 * gr];
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e)
@@ -471,11 +466,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
         }
         for (int j = 0; j < n; ++j, ++kt, ++mine) {
           ok = __all_sync(0xffffffffu, mbar_wait(&ct.s_full[st], mine & 1, abort) &&
-                                           mbar_wait(&ct.scale_full[kt & 1], (kt >> 1) & 1, abort));
+                                           mbar_wait(&ct.scale_full[kt & 3], (kt >> 2) & 1, abort));
           if (!ok) break;
-          const float sc = fmaxf(row_scale * ct.k_scale[kt & 1], 0x1p-126f);  // not 0: it meets -inf below
-          const uint32_t have = ct.have[kt & 1];
-          const int v_new = ct.v_exp[kt & 1], tok = (from + j) * TK;
+          const float sc = fmaxf(row_scale * ct.k_scale[kt & 3], 0x1p-126f);  // not 0: it meets -inf below
+          const uint32_t have = ct.have[kt & 3];
+          const int v_new = ct.v_exp[kt & 3], tok = (from + j) * TK;
           tc_fence_after();
           float sv[128];
           {
@@ -604,7 +599,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
     const int g = lane >> 2, c = lane & 3;
     const int row8 = 8 * w4 + ((g & 1) ? 4 + ((g >> 1) ^ 1) : g >> 1);  // reads and writes without bank conflicts
     uint32_t* k_const = reinterpret_cast<uint32_t*>(smem + S::CONST);
-    uint32_t* v_const = k_const + TK * NG;
     const int copy16 = min(a.c.page_shift, 7) - 4;  // log2 of a copy's blocks
     // the four warps stay in step, a wait that gave up in one thread ends all: every thread passes the same barriers
     const auto sync_deq = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
@@ -656,38 +650,44 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       const int ke = min(max(all4(ct.warp_exp[0]), -119), 110);
       v_exp = max(v_exp, min(max(all4(ct.warp_exp[1]), -119), 110));
       const float kn = pow2(-ke), vn = pow2(-v_exp);
-      float lo[NG];
+      uint32_t* v_const = k_const + (1 + (kt & 1)) * TK * NG;
+      float mid[NG];
 #pragma unroll
       for (int gr = 0; gr < NG; ++gr) {
-        const float step = bf_lo(kw[gr]), step_a = __uint_as_float((kw[gr] << 16) & 0xfffe0000u);
-        k_const[d * NG + gr] = half2_bits(step_a * kn * 16777216.f, (step - step_a) * kn * 16777216.f);
+        const float step = bf_lo(kw[gr]) * kn;
+        k_const[d * NG + gr] = half2_bits(step * 16777216.f, -8.f * step);
         v_const[d * NG + gr] = half2_bits(bf_lo(vw[gr]) * vn * 16777216.f, bf_hi(vw[gr]) * vn);
-        lo[gr] = bf_hi(kw[gr]) * kn;
+        mid[gr] = fmaf(8.f, step, bf_hi(kw[gr]) * kn);
       }
       if (d == 0) {
         uint32_t have = 0;
         for (int b = 0; b < TK / 16; ++b)
           have |= (uint32_t)(tile * TK + 16 * b >= seen || (made >> (b >> copy16) & 1u)) << b;
-        ct.have[kt & 1] = have;
-        ct.k_scale[kt & 1] = pow2(ke);
-        ct.v_exp[kt & 1] = v_exp;
-        mbar_arrive(&ct.scale_full[kt & 1]);
+        // the place of the tile before the three last: every row has handed that one's P on
+        ct.have[kt & 3] = have;
+        ct.k_scale[kt & 3] = pow2(ke);
+        ct.v_exp[kt & 3] = v_exp;
+        mbar_arrive(&ct.scale_full[kt & 3]);
       }
       sync_deq();
-      if (!there || (kt >= 1 && !mbar_wait(&ct.k_empty, (kt - 1) & 1, abort))) return false;
-      uint8_t* dst = smem + S::K;
+      if (!there || (kt >= 2 && !mbar_wait(&ct.k_empty[kt & 1], ((kt >> 1) - 1) & 1, abort))) return false;
+      uint8_t* dst = smem + S::K + (kt & 1) * Q_BYTES;
       {
-        float col[16];
+        float col[16];  // against the sums' parts: first, first, second
 #pragma unroll
-        for (int e = 0; e < 16; ++e) col[e] = e < 3 * NG ? lo[e / 3 < NG ? e / 3 : 0] : 0.f;
+        for (int e = 0; e < 16; ++e) col[e] = 0.f;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          col[3 * gr] = col[3 * gr + 1] = __half2float(__float2half_rn(mid[gr]));
+          col[3 * gr + 2] = mid[gr] - col[3 * gr];
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<uint4*>(dst + 2 * OPERAND + sw32_offset(d, e)) =
+          *reinterpret_cast<uint4*>(dst + OPERAND + sw32_offset(d, e)) =
               make_uint4(half2_bits(col[8 * e], col[8 * e + 1]), half2_bits(col[8 * e + 2], col[8 * e + 3]),
                          half2_bits(col[8 * e + 4], col[8 * e + 5]), half2_bits(col[8 * e + 6], col[8 * e + 7]));
       }
-      const __half2 zero = __float2half2_rn(0.f), sixteenth = __float2half2_rn(0.0625f);
-#pragma unroll 1
+#pragma unroll DEQ_UNROLL
       for (int p = 0; p < 4; ++p) {
         const int r = 32 * p + row8;
         const uint4 x = *reinterpret_cast<const uint4*>(raw + (r >> 4) * Blk::BYTES + 64 * (r & 15) + 16 * c);
@@ -695,37 +695,46 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const __half2 k = *reinterpret_cast<const __half2*>(&k_const[r * NG + i * NG / 4]);
-          const __half2 sa = __low2half2(k), sb = __high2half2(k);
-          uint8_t* to = dst + (i >> 1) * ATOM + r * 128 + (((4 * (i & 1) + c) ^ (r & 7)) << 4);
-          *reinterpret_cast<uint4*>(to) = widen8(w[i], sa, __hmul2(sa, sixteenth), zero);
-          *reinterpret_cast<uint4*>(to + OPERAND) = widen8(w[i], sb, __hmul2(sb, sixteenth), zero);
+          const __half2 st = __low2half2(k);
+          *reinterpret_cast<uint4*>(dst + (i >> 1) * ATOM + r * 128 + (((4 * (i & 1) + c) ^ (r & 7)) << 4)) =
+              widen8(w[i], st, __hmul2(st, __float2half2_rn(0.0625f)), __high2half2(k));
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(&ct.k_full);
+      mbar_arrive(&ct.k_full[kt & 1]);
       return true;
+    };
+    // the codes of a tile's values, taken out of its blocks ahead of their turn (the blocks' place is free then)
+    uint4 v_codes[4];
+    const auto take_values = [&](uint32_t kt) {
+      const uint8_t* raw = smem + S::RAW + (kt & 1) * S::TILE + Blk::V_CODES;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const int r = 32 * p + row8;
+        v_codes[p] = *reinterpret_cast<const uint4*>(raw + (r >> 4) * Blk::BYTES + 64 * (r & 15) + 16 * c);
+      }
+      mbar_arrive(&ct.raw_empty[kt & 1]);
     };
     const auto values = [&](uint32_t kt) {
       if (kt >= 1 && !mbar_wait(&ct.v_empty, (kt - 1) & 1, abort)) return false;
-      const uint8_t* raw = smem + S::RAW + (kt & 1) * S::TILE;
+      const uint32_t* v_const = k_const + (1 + (kt & 1)) * TK * NG;
       uint8_t* dst = smem + S::V;
-#pragma unroll 1
+#pragma unroll
       for (int p = 0; p < 4; ++p) {
         const int r = 32 * p + row8, u = c ^ (kv4_v_swizzle(r & 15) >> 1);
-        const uint4 x = *reinterpret_cast<const uint4*>(raw + (r >> 4) * Blk::BYTES + Blk::V_CODES + 64 * (r & 15) + 16 * c);
+        const uint4 x = v_codes[p];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const __half2 k = *reinterpret_cast<const __half2*>(&v_const[r * NG + i * NG / 4]);
-          const __half2 st = __low2half2(k), st20 = __hmul2(st, __float2half2_rn(0.0625f));
+          const __half2 st = __low2half2(k);
           const uint32_t w = i < 2 ? __byte_perm(x.x, x.z, (i & 1) ? 0x7632 : 0x5410)
                                    : __byte_perm(x.y, x.w, (i & 1) ? 0x7632 : 0x5410);
           *reinterpret_cast<uint4*>(dst + (i >> 1) * ATOM + r * 128 + (((4 * (i & 1) + u) ^ (r & 7)) << 4)) =
-              widen8(w, st, st20, __high2half2(k));
+              widen8(w, st, __hmul2(st, __float2half2_rn(0.0625f)), __high2half2(k));
         }
       }
       fence_proxy_async_smem();
       mbar_arrive(&ct.v_full);
-      mbar_arrive(&ct.raw_empty[kt & 1]);
       return true;
     };
     uint32_t kt = 0, segs = 0;
@@ -741,10 +750,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       if (d < 4) ct.nan_from[ring][d] = 0x7fffffff;
       sync_deq();
       v_exp = -119;
-      // keys and values have one buffer each: keys free once both streams' scores are, values once both P V are
+      // K(0), then K(j + 1), V(j): values have one buffer, free once both streams' P V before are done
+      ok = all_deq(keys(s, from, kt, ring));
+      if (ok) take_values(kt);
       for (int j = 0; j < n && ok; ++j, ++kt) {
-        ok = all_deq(keys(s, from + j, kt, ring));
-        if (ok) ok = all_deq(values(kt));  // the constants are free then
+        if (j + 1 < n) ok = all_deq(keys(s, from + j + 1, kt + 1, ring));
+        if (ok) ok = all_deq(values(kt));
+        if (ok && j + 1 < n) take_values(kt + 1);
       }
     }
   }
@@ -806,11 +818,11 @@ __global__ void __launch_bounds__(JOIN_THREADS) kv4_prompt_join_kernel(const Att
 template <int NG>
 cudaError_t launch(const AttendArgs& a, int dev, cudaStream_t st) {
   using S = PromptSmem<NG>;
-  static_assert(S::CUM + (KV4_MAX_B + 1) * 4 <= 226 * 1024, "shared memory of one CTA");
+  static_assert(S::CUM + (KV4_PROMPT_MAX_B + 1) * 4 <= 227 * 1024, "shared memory of one CTA");
   static std::atomic<uint64_t> ready{0};
   if (device_pending(ready, dev)) {
     const cudaError_t e = cudaFuncSetAttribute(kv4_prompt_kernel<NG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               S::CUM + (KV4_MAX_B + 1) * 4);
+                                               S::CUM + (KV4_PROMPT_MAX_B + 1) * 4);
     if (e != cudaSuccess) return e;
     mark_device(ready, dev);
   }
