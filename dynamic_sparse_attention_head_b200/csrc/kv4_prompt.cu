@@ -127,6 +127,12 @@ __device__ __forceinline__ int fold_units(int32_t n, int32_t kv, int32_t group, 
   return max((int)max(sum, (int64_t)0), top) + 2;
 }
 
+// units of a KV head: whole folds, and the middle pair of an odd number, which is alone
+__device__ __forceinline__ int64_t head_units(int32_t n, int32_t kv, int32_t group, int rts) {
+  return (int64_t)(rts / 2) * fold_units(n, kv, group, rts) +
+         (rts & 1 ? tiles_of(n, kv, group, rts / 2) + 1 : 0);
+}
+
 // Running sum of the requests' units into cum [B + 1]; returns the total (above 2^31: too many).
 __device__ __forceinline__ int64_t scan_units(const AttendArgs& a, int32_t* cum, int64_t* sums, int* bad) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
@@ -139,7 +145,7 @@ __device__ __forceinline__ int64_t scan_units(const AttendArgs& a, int32_t* cum,
       int32_t q0, n, kv;
       if (!request_lens(a, b, q0, n, kv)) *bad = 1;
       const int rts = pairs_of(n, a.group);
-      if (rts) x = (int64_t)a.c.Hkv * ((rts + 1) / 2) * fold_units(n, kv, a.group, rts);
+      if (rts) x = (int64_t)a.c.Hkv * head_units(n, kv, a.group, rts);
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -167,15 +173,12 @@ __device__ __forceinline__ PairSeg locate(const AttendArgs& a, const int32_t* cu
   }
   s.b = lo;
   request_lens(a, lo, s.q0, s.n, s.kv);
-  const int rts = pairs_of(s.n, a.group), folds = (rts + 1) / 2;
-  const int units = fold_units(s.n, s.kv, a.group, rts);
-  const int i = (t - cum[lo]) / units;
-  s.h = i / folds;
-  const int f = i - s.h * folds, base = cum[lo] + i * units;
+  const int rts = pairs_of(s.n, a.group), units = fold_units(s.n, s.kv, a.group, rts);
+  const int per_head = (int)head_units(s.n, s.kv, a.group, rts);
+  s.h = (t - cum[lo]) / per_head;
+  const int in_head = t - cum[lo] - s.h * per_head, f = in_head / units, base = t - in_head + f * units;
   const int ta = tiles_of(s.n, s.kv, a.group, f);
-  if (2 * f + 1 == rts) {  // the middle pair is alone
-    s.rt = f, s.first = base, s.count = units, s.tiles = ta;
-  } else if (t - base <= ta) {
+  if (f == rts / 2 || t - base <= ta) {  // the middle pair, or a fold's first
     s.rt = f, s.first = base, s.count = ta + 1, s.tiles = ta;
   } else {
     s.rt = rts - 1 - f, s.first = base + ta + 1, s.count = units - ta - 1;
