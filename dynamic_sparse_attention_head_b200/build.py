@@ -33,7 +33,7 @@ def _binding_command():
            sysconfig.get_paths()["include"]]
     # libmsa.so lies beside it; torch's libraries are loaded when serving.py imports torch first
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", *(f"-I{i}" for i in inc),
-            os.path.join(CSRC, "binding.cpp"), "-o", BINDING, LIB, "-Wl,-rpath,$ORIGIN",
+            os.path.join(CSRC, "binding.cpp"), "-o", BINDING, f"-L{HERE}", "-l:libmsa.so", "-Wl,-rpath,$ORIGIN",
             *(f"-L{d}" for d in cpp_extension.library_paths()), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
 
 

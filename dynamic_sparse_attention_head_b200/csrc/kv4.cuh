@@ -43,10 +43,15 @@ struct AttendArgs {
   const int32_t *table, *kv_lens, *cu_q;
   int64_t table_stride;
   int32_t max_blocks, B, total_q, Hq, group;  // group: query heads of a KV head
+  uint32_t group_mul;                         // x / group = (x group_mul) >> (31 + group_shift)
+  int32_t group_shift;
   float scale2;                               // softmax scale * log2(e)
   float* lse;
   uint32_t* arrivals;  // [KV4_MAX_CTAS]
   float* partial;      // results of segments over several CTAs
+  __device__ __forceinline__ int by_group(int x) const {
+    return (int)(((uint64_t)(uint32_t)x * group_mul) >> (31 + group_shift));
+  }
   float* heads;        // [KV4_MAX_CTAS][warp][rows][128]: results of segments that began in a warp before
 };
 

@@ -109,6 +109,52 @@ __device__ __forceinline__ int row_tiles(int32_t n, int32_t group) {
   return (int)(((int64_t)n * group + 8 * NT - 1) / (8 * NT));
 }
 
+__device__ __forceinline__ float weight_of(float x, float top) { return x == NEG_INF ? 0.f : ex2(x - top); }
+
+// Adds U partial results (maximum and sum st, four channels y) to (top, sum, x).
+template <int U>
+__device__ __forceinline__ void add_parts(float& top, float& sum, float4& x, const float2 (&st)[U], const float4 (&y)[U]) {
+  float up = top;
+#pragma unroll
+  for (int u = 0; u < U; ++u) up = fmaxf(up, st[u].x);
+  const float f0 = weight_of(top, up);
+  top = up;
+  sum *= f0;
+  x.x *= f0, x.y *= f0, x.z *= f0, x.w *= f0;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float f = weight_of(st[u].x, top);
+    sum = fmaf(st[u].y, f, sum);
+    x.x = fmaf(y[u].x, f, x.x), x.y = fmaf(y[u].y, f, x.y), x.z = fmaf(y[u].z, f, x.z), x.w = fmaf(y[u].w, f, x.w);
+  }
+}
+
+// units of a segment: its tiles (2^shift keys each), and one for what its start and end cost
+__device__ __forceinline__ int units_of(int kv, int shift) {
+  return 1 + (int)(((int64_t)kv + (1 << shift) - 1) >> shift);
+}
+
+// The segment that holds unit t.  Out of line: a launch of few tiles is bound by fetching its code.
+template <int NT>
+__device__ __noinline__ Segment segment_at(const AttendArgs& a, const int32_t* cum, int shift, int t) {
+  Segment s;
+  int lo = 0, hi = a.B;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (cum[m] <= t) lo = m;
+    else hi = m;
+  }
+  s.b = lo;
+  request_lens(a, lo, s.q0, s.n, s.kv);
+  s.count = units_of(s.kv, shift);
+  const int i = (t - cum[lo]) / s.count;
+  const int rts = row_tiles<NT>(s.n, a.group);
+  s.h = rts == 1 ? i : i / rts;
+  s.rt = i - s.h * rts;
+  s.first = cum[lo] + i * s.count;
+  return s;
+}
+
 template <int NG, int NT, int TK, int W, int STAGES>
 struct AttendSmem {
   static constexpr int TILE = TK / 16 * Kv4Block<NG>::BYTES;
@@ -123,12 +169,11 @@ struct AttendSmem {
   static_assert(BARS % 8 == 0 && CUM % 4 == 0, "alignment");
 };
 
-template <int NG, int NT, int TK, int CK, int W, int STAGES>
-__global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs a) {
+template <int NG, int NT, int TK, int W, int STAGES>
+__global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const __grid_constant__ AttendArgs a) {
   using S = AttendSmem<NG, NT, TK, W, STAGES>;
   using Blk = Kv4Block<NG>;
   constexpr int ROWS = 8 * NT;
-  constexpr int MT = CK / 16;  // operand tiles of 16 keys in one pass
   constexpr int THREADS = W * 32;
   extern __shared__ __align__(128) uint8_t smem[];
   float* heads = a.heads + (int64_t)blockIdx.x * W * ROWS * HD;  // [W][ROWS][HD]
@@ -136,85 +181,83 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
   Segment* segs = reinterpret_cast<Segment*>(smem + S::SEGS);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BARS);
   int32_t* cum = reinterpret_cast<int32_t*>(smem + S::CUM);
-  __shared__ int64_t sums[W];
-  __shared__ int abort_flag, bad, last_of[2];
-  __shared__ uint8_t ends[W];  // 1: has a head, 2: the head's segment ends in the stretch, 4: has a tail
+  __shared__ int abort_flag, bad, last_of[2], line_total, line_shift;
+  // 1: has a head, 2: the head's segment ends in the stretch, 4: has a tail, 8: the head is in the workspace
+  __shared__ uint8_t ends[W];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
-  if (tid == 0) {
-    abort_flag = 0;
-    bad = 0;
-    cum[0] = 0;
-    for (int i = 0; i < W * STAGES; ++i) mbar_init(bars + i, 1);
-    fence_barrier_init();
-  }
-  __syncthreads();
+  if (tid < W * STAGES) mbar_init(bars + tid, 1);
+  if (tid == 0) abort_flag = 0;
+  fence_barrier_init();
 
-  // ---- the line of units: running sum of the requests' counts ----
-  const auto units_of = [](int kv) { return 1 + (kv + TK - 1) / TK; };
-  int64_t run = 0;
-  for (int b0 = 0; b0 < a.B; b0 += THREADS) {
-    const int b = b0 + tid;
-    int64_t x = 0;
-    if (b < a.B) {
-      int32_t q0, n, kv;
-      if (!request_lens(a, b, q0, n, kv)) bad = 1;
-      x = (int64_t)row_tiles<NT>(n, a.group) * a.c.Hkv * units_of(kv);
+  // ---- the line of units: running sum of the requests' counts, by one warp ----
+  // A unit is a tile of TK keys; or 16 keys, where that still leaves every warp less than a tile: short
+  // contexts then spread over more warps.
+  if (warp == 0) {
+    uint32_t cut = 0;
+    uint64_t blocks = 0;  // of 16 keys
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      int32_t q0, n = 0, kv = 0;
+      if (b0 + lane < a.B && !request_lens(a, b0 + lane, q0, n, kv)) cut = 1;
+      blocks += (uint64_t)row_tiles<NT>(n, a.group) * a.c.Hkv * ((kv + 15) >> 4);
     }
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+    for (int o = 16; o > 0; o >>= 1) blocks += __shfl_xor_sync(0xffffffffu, blocks, o);
+    cut = __any_sync(0xffffffffu, cut);
+    const int shift = blocks < (uint64_t)gridDim.x * W * (TK / 16) ? 4 : (TK == 64 ? 6 : 5);
+    uint64_t run = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      int32_t q0, n = 0, kv = 0;
+      if (b0 + lane < a.B) request_lens(a, b0 + lane, q0, n, kv);
+      uint64_t x = (uint64_t)row_tiles<NT>(n, a.group) * a.c.Hkv * (uint32_t)units_of(kv, shift);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      x += run;
+      if (b0 + lane < a.B) cum[b0 + lane + 1] = (int32_t)min(x, (uint64_t)0x7fffffff);
+      run = __shfl_sync(0xffffffffu, x, 31);
     }
-    if (lane == 31) sums[warp] = x;
-    __syncthreads();
-    int64_t before = run;
-    for (int w = 0; w < warp; ++w) before += sums[w];
-    if (b < a.B) cum[b + 1] = (int32_t)min(before + x, (int64_t)0x7fffffff);
-    for (int w = 0; w < W; ++w) run += sums[w];
-    __syncthreads();
+    if (lane == 0) {
+      cum[0] = 0;
+      line_total = run > 0x7fffffff ? -1 : (int)run;  // -1: more units than the line has numbers for
+      line_shift = shift;
+      bad = 0;
+      if (blockIdx.x == 0 && (cut || run > 0x7fffffff)) atomicOr(a.c.state, DEV_ERR_BOUNDS);
+    }
   }
-  if (blockIdx.x == 0 && tid == 0 && (bad || run > 0x7fffffff)) atomicOr(a.c.state, DEV_ERR_BOUNDS);
-  if (run > 0x7fffffff) return;  // more units than the line has numbers for
-  const int total = (int)run;
+  __syncthreads();
+  const int total = line_total, unit_shift = line_shift;
   // a CTA takes at least a unit per warp where there are that many
   const int active = min((int)gridDim.x, max(1, (total + W - 1) / W));
-  if ((int)blockIdx.x >= active || total == 0) return;
+  if ((int)blockIdx.x >= active || total <= 0) return;
   const auto edge = [&](int i) { return (int)((int64_t)total * i / active); };
   const int t0 = edge(blockIdx.x), t1 = edge(blockIdx.x + 1);
   const int w0 = t0 + (int)((int64_t)(t1 - t0) * warp / W), w1 = t0 + (int)((int64_t)(t1 - t0) * (warp + 1) / W);
 
-  const auto locate = [&](int t) {  // the segment that holds unit t
-    Segment s;
-    int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-      const int m = (lo + hi) >> 1;
-      if (cum[m] <= t) lo = m;
-      else hi = m;
-    }
-    s.b = lo;
-    request_lens(a, lo, s.q0, s.n, s.kv);
-    s.count = units_of(s.kv);
-    const int i = (t - cum[lo]) / s.count;
-    const int rts = row_tiles<NT>(s.n, a.group);
-    s.h = i / rts;
-    s.rt = i - s.h * rts;
-    s.first = cum[lo] + i * s.count;
-    return s;
-  };
+  const auto locate = [&](int t) { return segment_at<NT>(a, cum, unit_shift, t); };
   // keys that the last row of the segment's tile sees (none: <= 0)
   const auto seen_by_last = [&](const Segment& s) {
     const int last_row = min((s.rt + 1) * ROWS, s.n * a.group) - 1;
-    return s.kv - s.n + last_row / a.group + 1;
+    return s.kv - s.n + a.by_group(last_row) + 1;
   };
 
   // ---- this warp's ring: the tiles of its stretch in order, across segments ----
   uint8_t* ring = smem + S::RING + warp * STAGES * S::TILE;
   uint64_t* bar = bars + warp * STAGES;
-  // a copy is a page's part of the tile, or the tile: `per` copies a tile, `copy_shift` tokens each
-  const int copy_shift = min(a.c.page_shift, TK == 64 ? 6 : 5);
-  const int per = TK >> copy_shift;
+  // a copy is a page's part of the unit, or the unit: `per` copies a unit, 2^copy_shift tokens each
+  const int copy_shift = min(a.c.page_shift, unit_shift), per = 1 << (unit_shift - copy_shift);
+  const Segment first_seg = w0 < w1 ? locate(w0) : Segment{};
+  if (w0 < w1) {  // its queries, on their way while the first tiles are looked up
+    const int r = first_seg.rt * ROWS + lane % ROWS, token = min(a.by_group(r), first_seg.n - 1);
+    const int hd = first_seg.h * a.group + r - a.by_group(r) * a.group;
+    const __nv_bfloat16* q = a.Q + (int64_t)hd * a.q_head + (int64_t)(first_seg.q0 + token) * a.q_row;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(q + (lane / ROWS) * (HD * ROWS / 32)));
+  }
   Segment ps;
   ps.first = w0;
   ps.count = 0;
@@ -228,12 +271,12 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
     while (p_tile >= p_end) {  // on to the next segment of the stretch
       const int at = ps.first + ps.count;
       if (at >= w1) return;
-      ps = locate(at);
+      ps = at == w0 ? first_seg : locate(at);
       p_seen = seen_by_last(ps);
       // unit 0 of a segment carries no keys; tiles behind the last row's keys are not needed
       p_tile = max(at, w0) - ps.first - 1;
       p_tile = max(p_tile, 0);
-      p_end = min(min(ps.first + ps.count, w1) - ps.first - 1, (p_seen + TK - 1) / TK);
+      p_end = min(min(ps.first + ps.count, w1) - ps.first - 1, max(units_of(p_seen, unit_shift) - 1, 0));
       entry_ok = false;
     }
     const int first = p_tile * per;
@@ -269,9 +312,9 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
   uint32_t k1024;  // fp16 1024 twice, kept in a register
   asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k1024));
   const int key_of = (g & 1) ? 4 + ((g >> 1) ^ 1) : g >> 1;  // key of operand row g, in 8
-  const auto weight = [](float x, float top) { return x == NEG_INF ? 0.f : ex2(x - top); };
-  const auto write_row = [&](const Segment& s, int r, int ch, float4 x, float top, float sum) {
-    const int rc = s.rt * ROWS + r, token = rc / a.group, hd = s.h * a.group + rc - token * a.group;
+  // four channels of row `rc` (token * group + head) of a segment
+  const auto write_row = [&](const Segment& s, int rc, int token, int ch, float4 x, float top, float sum) {
+    const int hd = s.h * a.group + rc - token * a.group;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     uint2 w;
     w.x = pack_bf16x2(x.x * inv, x.y * inv);
@@ -283,16 +326,16 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
   if (lane == 0) ends[warp] = 0;
 
   for (int at = w0; at < w1;) {
-    const Segment s = locate(at);
+    const Segment s = at == w0 ? first_seg : locate(at);
     const int s_end = min(s.first + s.count, w1);
     const int seen = seen_by_last(s);
     const int row0 = s.rt * ROWS, rows = min(ROWS, s.n * a.group - row0);
-    const int seen_first = s.kv - s.n + row0 / a.group + 1;
+    const int seen_first = s.kv - s.n + a.by_group(row0) + 1;
 
     // ---- queries: operand B of S^T, column g = row, scaled by a power of two into fp16 ----
     uint32_t qf[NT][8][2];
     float qs[NG][NT][2];
-    int lim[NT][2];
+    int lim[NT][2], token_of[NT][2];
     float to_score;
     {
       uint4 raw[NT][4];
@@ -301,7 +344,7 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
       for (int nt = 0; nt < NT; ++nt) {
         const int r = row0 + nt * 8 + g;
         const bool live = nt * 8 + g < rows;
-        const int tok = live ? r / a.group : 0, hd = live ? r - tok * a.group : 0;
+        const int tok = live ? a.by_group(r) : 0, hd = live ? r - tok * a.group : 0;
         const __nv_bfloat16* q = a.Q + (int64_t)(s.h * a.group + hd) * a.q_head + (int64_t)(s.q0 + tok) * a.q_row;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -313,7 +356,8 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int rc = row0 + nt * 8 + 2 * c + e;
-          lim[nt][e] = nt * 8 + 2 * c + e < rows ? s.kv - s.n + rc / a.group + 1 : s.kv;
+          token_of[nt][e] = a.by_group(rc);
+          lim[nt][e] = nt * 8 + 2 * c + e < rows ? s.kv - s.n + token_of[nt][e] + 1 : s.kv;
         }
       }
 #pragma unroll
@@ -372,10 +416,10 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
       }
     }
 
-    // CK keys of a tile, from its key `in_tile` on.  PARTIAL: some keys are hidden, from all rows (behind the last row's, or on no page)
-    // or from some.
-    const auto tile_pass = [&](auto partial_tag, const uint8_t* kb, int tok, int in_tile, uint32_t have) {
+    // 16 MT keys from `tok` on.  PARTIAL: some are hidden, from all rows (behind the last row's) or from some.
+    const auto tile_pass = [&](auto partial_tag, auto mt_tag, const uint8_t* kb, int tok) {
       constexpr bool PARTIAL = decltype(partial_tag)::value;
+      constexpr int MT = decltype(mt_tag)::value;
       float sc[MT][NT][4];
       uint32_t vsw[MT][2][NG];
       float vmax = 0.f, top[NT][2];
@@ -408,7 +452,7 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int key = tok + 16 * mt + 8 * r + key_of;
-          const bool shown = !PARTIAL || (key < seen && ((have >> ((in_tile + 16 * mt) >> copy_shift)) & 1u));
+          const bool shown = !PARTIAL || key < seen;
           uint32_t ksw[NG];
           const uint32_t* kp = reinterpret_cast<const uint32_t*>(blk + Blk::K_SCALES + 4 * NG * (key_of + 8 * r));
           const uint32_t* vp = reinterpret_cast<const uint32_t*>(blk + Blk::V_SCALES + 4 * NG * (key_of + 8 * r));
@@ -527,17 +571,19 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
       }
     };
 
-    const int tiles = min(s_end - s.first - 1, (seen + TK - 1) / TK);
+    const int tiles = min(s_end - s.first - 1, max(units_of(seen, unit_shift) - 1, 0));
     for (int tile = max(at - s.first - 1, 0); tile < tiles; ++tile) {
       const bool there = mbar_wait(bar + c_stage, c_parity, &abort_flag);
       const uint8_t* kb = ring + c_stage * S::TILE;
       const uint32_t all = (1u << per) - 1, have = there ? (holds >> (4 * c_stage)) & all : 0u;
-      const int tok = tile * TK;
+      const int tok = tile << unit_shift;
+      if ((1 << unit_shift) == TK && have == all && tok + TK <= seen_first) {
+        tile_pass(std::false_type{}, std::integral_constant<int, TK / 16>{}, kb, tok);
+      } else {
 #pragma unroll 1
-      for (int k = 0; k < TK; k += CK) {
-        const uint8_t* at_k = kb + k / 16 * Blk::BYTES;
-        if (have == all && tok + k + CK <= seen_first) tile_pass(std::false_type{}, at_k, tok + k, k, have);
-        else if (have && tok + k < seen) tile_pass(std::true_type{}, at_k, tok + k, k, have);
+        for (int b = 0; b < 1 << (unit_shift - 4); ++b)
+          if ((have >> (16 * b >> copy_shift) & 1u) && tok + 16 * b < seen)
+            tile_pass(std::true_type{}, std::integral_constant<int, 1>{}, kb + b * Blk::BYTES, tok + 16 * b);
       }
       __syncwarp();  // every lane has read the stage
       --in_flight;
@@ -558,9 +604,10 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
         }
     const float of = vtop * 0.0078125f;  // 1 / 128
     const bool starts = s.first >= w0, stops = s.first + s.count <= w1;
-    // a head (it began in a stretch before) goes to the workspace, a tail into the ring, which is
-    // empty then: a tail is a stretch's last segment
-    float* mine = starts ? reinterpret_cast<float*>(ring) : heads + warp * ROWS * HD;
+    // a head (it began in a stretch before) or a tail goes into the ring where it is the stretch's last
+    // segment and the ring empty; a head before others goes to the workspace
+    const bool last = s_end == w1;
+    float* mine = last ? reinterpret_cast<float*>(ring) : heads + warp * ROWS * HD;
     float* mine_st = stats + (2 * warp + (starts ? 1 : 0)) * ROWS * 2;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -575,7 +622,7 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
                                        fmaf(o[2 * q + 1][nt][e], of, zq),
                                        fmaf(o[2 * q + 1][nt][2 + e], of * 0.0625f, zq));
           if (starts && stops) {
-            if (r < rows) write_row(s, r, 32 * q + 4 * g, x, top, l[nt][e]);
+            if (r < rows) write_row(s, row0 + r, token_of[nt][e], 32 * q + 4 * g, x, top, l[nt][e]);
           } else {
             *reinterpret_cast<float4*>(mine + r * HD + 32 * q + 4 * g) = x;
           }
@@ -584,7 +631,7 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
       }
     if (lane == 0) {
       if (!starts) {
-        ends[warp] |= stops ? 3 : 1;
+        ends[warp] |= 1 | (stops ? 2 : 0) | (last ? 0 : 8);
         if (w0 == t0) segs[W] = s;
       } else if (!stops) {
         ends[warp] |= 4;
@@ -606,38 +653,49 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
   const auto owner = [&](int t) { return (int)((((int64_t)t + 1) * active - 1) / total); };
   uint32_t crosses = 0;  // bit 0: the CTA's head, bit 1: its tail, in the workspace
   Segment cross_seg[2];
+  uint32_t has_head = 0, stops_in = 0, has_tail = 0, in_ws = 0;  // a bit per warp
+  {
+    const uint32_t e = lane < W ? ends[lane] : 0u;
+    has_head = __ballot_sync(0xffffffffu, e & 1);
+    stops_in = __ballot_sync(0xffffffffu, e & 2);
+    has_tail = __ballot_sync(0xffffffffu, e & 4);
+    in_ws = __ballot_sync(0xffffffffu, e & 8);
+  }
   int lead = 0;  // the first warp with a stretch
   while ((int64_t)(t1 - t0) * (lead + 1) / W == 0) ++lead;
-  for (int first = -1; first < W; ++first) {
-    if (first < 0 ? !(ends[lead] & 1) : !(ends[first] & 4)) continue;
+#pragma unroll 1
+  for (uint32_t starts = has_tail << 1 | (has_head >> lead & 1); starts; starts &= starts - 1) {
+    const int first = __ffs(starts) - 2;  // -1: the CTA's head
     const Segment s = segs[first < 0 ? W : first];
-    int last = first < 0 ? lead : first;
-    bool open = first >= 0 || !(ends[lead] & 2);
-    for (int w = last + 1; w < W && open; ++w) {
-      if (!(ends[w] & 1)) continue;  // a warp without a stretch
-      last = w;
-      open = !(ends[w] & 2);
-    }
+    // the heads after it, up to the one whose segment ends (warps without a stretch have none)
+    const uint32_t after = has_head & ~((first < 0 ? 1u << lead : 2u << first) - 1), end = after & stops_in;
+    const uint32_t members = (end ? after & (end ^ (end - 1)) : after) | (first < 0 ? 0u : 1u << first);
     const bool whole = s.first >= t0 && s.first + s.count <= t1;
     const int which = s.first >= t0 ? 1 : 0, rows = min(ROWS, s.n * a.group - s.rt * ROWS);
+#pragma unroll 1
     for (int i = tid; i < rows * (HD / 4); i += THREADS) {
       const int r = i / (HD / 4), ch = (i % (HD / 4)) * 4;
-      const auto member = [&](int w) { return stats + (2 * w + (w == first ? 1 : 0)) * ROWS * 2 + 2 * r; };
-      const auto is_in = [&](int w) { return w == first || (ends[w] & 1); };
       float top = NEG_INF, sum = 0.f;
-      for (int w = max(first, 0); w <= last; ++w)
-        if (is_in(w)) top = fmaxf(top, member(w)[0]);
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = max(first, 0); w <= last; ++w) {
-        if (!is_in(w)) continue;
-        const float* src = w == first ? reinterpret_cast<const float*>(smem + S::RING + w * STAGES * S::TILE) : heads + w * ROWS * HD;
-        const float4 y = *reinterpret_cast<const float4*>(src + r * HD + ch);  // heads: written by this CTA
-        const float f = weight(member(w)[0], top);
-        sum = fmaf(member(w)[1], f, sum);
-        x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
+      constexpr int U = 4;  // results read together
+      for (uint32_t left = members; left;) {
+        float2 st[U];
+        float4 y[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int w = left ? __ffs(left) - 1 : max(first, lead);
+          const float* src = w != first && (in_ws >> w & 1)
+                                 ? heads + w * ROWS * HD
+                                 : reinterpret_cast<const float*>(smem + S::RING + w * STAGES * S::TILE);
+          st[u] = *reinterpret_cast<const float2*>(stats + (2 * w + (w == first ? 1 : 0)) * ROWS * 2 + 2 * r);
+          y[u] = *reinterpret_cast<const float4*>(src + r * HD + ch);  // heads: written by this CTA
+          if (!left) st[u] = make_float2(NEG_INF, 0.f), y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          left &= left - 1;
+        }
+        add_parts(top, sum, x, st, y);
       }
       if (whole) {
-        write_row(s, r, ch, x, top, sum);
+        write_row(s, s.rt * ROWS + r, a.by_group(s.rt * ROWS + r), ch, x, top, sum);
       } else {
         float* dst = part(blockIdx.x, which);
         *reinterpret_cast<float4*>(dst + r * HD + ch) = x;
@@ -662,7 +720,7 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
       __threadfence();
     }
     __syncthreads();
-#pragma unroll
+#pragma unroll 1
     for (int which = 0; which < 2; ++which) {
       if (!(crosses >> which & 1) || !last_of[which]) continue;
       const Segment s = cross_seg[which];
@@ -671,19 +729,21 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
       for (int i = tid; i < rows * (HD / 4); i += THREADS) {
         const int r = i / (HD / 4), ch = (i % (HD / 4)) * 4;
         float top = NEG_INF, sum = 0.f;
-#pragma unroll 8
-        for (int k = from; k <= to; ++k) top = fmaxf(top, __ldcg(part(k, k == from) + MAX_ROWS * HD + 2 * r));
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int k = from; k <= to; ++k) {
-          const float* p = part(k, k == from);
-          const float2 st = __ldcg(reinterpret_cast<const float2*>(p + MAX_ROWS * HD + 2 * r));
-          const float4 y = __ldcg(reinterpret_cast<const float4*>(p + r * HD + ch));
-          const float f = weight(st.x, top);
-          sum = fmaf(st.y, f, sum);
-          x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
+        constexpr int U = 8;  // partial results on their way together
+        for (int k0 = from; k0 <= to; k0 += U) {
+          float2 st[U];
+          float4 y[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const float* p = part(min(k0 + u, to), k0 + u == from);
+            st[u] = __ldcg(reinterpret_cast<const float2*>(p + MAX_ROWS * HD + 2 * r));
+            y[u] = __ldcg(reinterpret_cast<const float4*>(p + r * HD + ch));
+            if (k0 + u > to) st[u] = make_float2(NEG_INF, 0.f), y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          add_parts(top, sum, x, st, y);
         }
-        write_row(s, r, ch, x, top, sum);
+        write_row(s, s.rt * ROWS + r, a.by_group(s.rt * ROWS + r), ch, x, top, sum);
       }
     }
   }
@@ -693,29 +753,29 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const AttendArgs 
   }
 }
 
-template <int NG, int NT, int TK, int CK, int W, int STAGES>
+template <int NG, int NT, int TK, int W, int STAGES>
 cudaError_t launch(const AttendArgs& a, int dev, cudaStream_t st) {
   using S = AttendSmem<NG, NT, TK, W, STAGES>;
   static_assert(S::CUM + (KV4_MAX_B + 1) * 4 <= 226 * 1024 + 512, "shared memory of one CTA");
   static_assert(8 * NT <= MAX_ROWS && W * 8 * NT <= MAX_WARP_ROWS, "rows of the results in the workspace");
   static std::atomic<uint64_t> ready{0};
   if (device_pending(ready, dev)) {
-    const cudaError_t e = cudaFuncSetAttribute(kv4_attend_kernel<NG, NT, TK, CK, W, STAGES>,
+    const cudaError_t e = cudaFuncSetAttribute(kv4_attend_kernel<NG, NT, TK, W, STAGES>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                S::CUM + (KV4_MAX_B + 1) * 4);
     if (e != cudaSuccess) return e;
     mark_device(ready, dev);
   }
   count_launches(1);
-  kv4_attend_kernel<NG, NT, TK, CK, W, STAGES>
+  kv4_attend_kernel<NG, NT, TK, W, STAGES>
       <<<std::min(sm_count(), KV4_MAX_CTAS), W * 32, S::CUM + (a.B + 1) * 4, st>>>(a);
   return cudaGetLastError();
 }
 
 template <int NG>
 cudaError_t launch_rows(const AttendArgs& a, int max_q, int dev, cudaStream_t st) {
-  if ((int64_t)max_q * a.group <= 8) return launch<NG, 1, 64, 64, (NG == 4 ? 8 : 12), 2>(a, dev, st);
-  return launch<NG, 2, 32, 32, 8, 3>(a, dev, st);
+  if ((int64_t)max_q * a.group <= 8) return launch<NG, 1, 64, NG == 4 ? 8 : 12, 2>(a, dev, st);
+  return launch<NG, 2, 32, 8, 3>(a, dev, st);
 }
 
 constexpr int PROMPT_ROWS = 64;  // query rows of a KV head from which on the tensor-memory kernel is taken
@@ -761,6 +821,12 @@ msa_status msa_kv4_attend(const msa_kv4_cache* cache, const void* Q, void* O, co
   a.q_head = strides->q_head, a.q_row = strides->q_row, a.o_head = strides->o_head, a.o_row = strides->o_row;
   a.table = block_table, a.kv_lens = kv_lens, a.cu_q = cu_q, a.table_stride = table_stride;
   a.max_blocks = max_blocks, a.B = B, a.total_q = total_q, a.Hq = Hq, a.group = Hq / cache->Hkv;
+  // x / group for 0 <= x < 2^31 as a product and a shift: with l = ceil(log2 group), 2^(31 + l) / group rounded up
+  // is off by less than 2^l / 2^(31 + l) of it (Granlund and Montgomery, 1994)
+  int l = 0;
+  while ((1 << l) < a.group) ++l;
+  a.group_mul = (uint32_t)(((1ull << (31 + l)) + a.group - 1) / a.group);
+  a.group_shift = l;
   a.scale2 = scale * LOG2E;
   a.lse = lse;
   a.arrivals = static_cast<uint32_t*>(ws);
