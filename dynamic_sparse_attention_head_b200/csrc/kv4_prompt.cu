@@ -196,6 +196,15 @@ __device__ __forceinline__ float* pair_part(const AttendArgs& a, int cta, int wh
   return a.partial + (2 * (int64_t)cta + which) * PAIR * PART;
 }
 
+// What a CTA leaves to the second kernel: the pair that began in its stretch and goes on behind it, up to
+// CTA `to` (-1: none).
+struct JoinInfo {
+  int32_t to, h, rt, n, q0, _pad[3];
+};
+__device__ __forceinline__ JoinInfo* join_info(const AttendArgs& a) {
+  return reinterpret_cast<JoinInfo*>(a.partial + (int64_t)KV4_MAX_CTAS * 2 * PAIR * PART);
+}
+
 __device__ __forceinline__ bool take_lock(int* lock, volatile int* abort) {
   for (int i = 0; atomicCAS(lock, 0, 1) != 0; ++i)
     if ((i & 63) == 63 && *abort) return false;
@@ -230,7 +239,7 @@ __device__ __forceinline__ uint4 widen8(uint32_t w, __half2 step24, __half2 step
 }
 
 template <int NG>
-__global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_constant__ AttendArgs a) {
   using S = PromptSmem<NG>;
   using Blk = Kv4Block<NG>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -264,6 +273,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
   __syncthreads();
   const int64_t run = scan_units(a, cum, ct.sums, &ct.bad);
   if (blockIdx.x == 0 && tid == 0 && (ct.bad || run > 0x7fffffff)) atomicOr(a.c.state, DEV_ERR_BOUNDS);
+  if (tid == 0) join_info(a)[blockIdx.x].to = -1;
   if (run > 0x7fffffff) return;  // more units than the line has numbers for
   const int total = (int)run, active = active_ctas(total, gridDim.x);
   if ((int)blockIdx.x >= active || total == 0) return;
@@ -410,7 +420,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       at = min(s.first + s.count, t1);
       const int from = tiles_from(s), n = max(tiles_to(s) - from, 0), rows = rows_of(s, st);
       const bool live = t < rows;
-      const int row = s.rt * PAIR + st * 128 + t, token = live ? row / a.group : 0;
+      const int row = s.rt * PAIR + st * 128 + t, token = live ? a.by_group(row) : 0;
       const int hd = s.h * a.group + (live ? row - token * a.group : 0);
       const int lim = live ? s.kv - s.n + token + 1 : 0x7fffffff;
       const int ring = segs & (NAN_RING - 1);
@@ -594,6 +604,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
       if (live && whole && a.lse)
         a.lse[(int64_t)hd * a.total_q + s.q0 + token] = l == 0.f ? NEG_INF : (m_used + log2f(l)) * (1.f / LOG2E);
       if (live && !whole) *reinterpret_cast<float2*>(part + HD) = make_float2(m_used, l);
+      if (st == 0 && t == 0 && !whole && s.first >= t0)
+        join_info(a)[blockIdx.x] = {line_owner(total, active, s.first + s.count - 1), s.h, s.rt, s.n, s.q0, {}};
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_DEQ));
@@ -775,47 +787,54 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const AttendArgs
   }
 }
 
-// Joins the rows of a pair that several CTAs worked on: block (i, j) takes rows 16 j .. of the pair that
-// began in CTA i's stretch and went on behind it.
-constexpr int JOIN_THREADS = 512, JOIN_ROWS = 16;
+// Joins the rows of a pair that several CTAs worked on: block (i, j) takes rows 64 j .. of the pair that
+// began in CTA i's stretch and went on behind it, a warp a row.
+constexpr int JOIN_THREADS = 512, JOIN_ROWS = 64;
 
-__global__ void __launch_bounds__(JOIN_THREADS) kv4_prompt_join_kernel(const AttendArgs a, int grid) {
-  extern __shared__ int32_t join_cum[];
-  __shared__ int64_t sums[JOIN_THREADS / 32];
-  __shared__ int bad;
-  const int64_t run = scan_units(a, join_cum, sums, &bad);
-  if (run > 0x7fffffff || run == 0) return;
-  const int total = (int)run, active = active_ctas(total, grid), cta = blockIdx.x;
-  if (cta >= active) return;
-  const int t0 = line_edge(total, active, cta), t1 = line_edge(total, active, cta + 1);
-  const PairSeg s = locate(a, join_cum, t1 - 1);
-  if (s.first < t0 || s.first + s.count <= t1) return;
-  const int to = line_owner(total, active, s.first + s.count - 1);
+__global__ void __launch_bounds__(JOIN_THREADS) kv4_prompt_join_kernel(const __grid_constant__ AttendArgs a) {
+  const int cta = blockIdx.x;
+  const JoinInfo s = join_info(a)[cta];
+  if (s.to < 0) return;
   const int rows = (int)min((int64_t)PAIR, (int64_t)s.n * a.group - (int64_t)s.rt * PAIR);
-  const int r = blockIdx.y * JOIN_ROWS + threadIdx.x / 32, ch = (threadIdx.x & 31) * 4;
-  if (r >= rows) return;
-  const auto part = [&](int k) { return pair_part(a, k, k == cta) + r * PART; };
-  float top = NEG_INF, sum = 0.f;
-#pragma unroll 4
-  for (int k = cta; k <= to; ++k) top = fmaxf(top, part(k)[HD]);
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = cta; k <= to; ++k) {
-    const float* p = part(k);
-    const float2 st = *reinterpret_cast<const float2*>(p + HD);
-    const float2 y0 = *reinterpret_cast<const float2*>(p + ch), y1 = *reinterpret_cast<const float2*>(p + ch + 2);
-    const float f = st.x == NEG_INF ? 0.f : ex2(st.x - top);
-    sum = fmaf(st.y, f, sum);
-    x.x = fmaf(y0.x, f, x.x), x.y = fmaf(y0.y, f, x.y), x.z = fmaf(y1.x, f, x.z), x.w = fmaf(y1.y, f, x.w);
+  const int lane = threadIdx.x & 31, ch = lane * 4;
+  for (int r = blockIdx.y * JOIN_ROWS + threadIdx.x / 32; r < min(rows, (int)(blockIdx.y + 1) * JOIN_ROWS);
+       r += JOIN_THREADS / 32) {
+    float top = NEG_INF, sum = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int U = 4;  // partial rows on their way together
+    for (int k0 = cta; k0 <= s.to; k0 += U) {
+      float2 st[U], y0[U], y1[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float* p = pair_part(a, min(k0 + u, s.to), k0 + u == cta) + r * PART;
+        st[u] = *reinterpret_cast<const float2*>(p + HD);
+        y0[u] = *reinterpret_cast<const float2*>(p + ch);
+        y1[u] = *reinterpret_cast<const float2*>(p + ch + 2);
+        if (k0 + u > s.to) st[u] = make_float2(NEG_INF, 0.f), y0[u] = y1[u] = make_float2(0.f, 0.f);
+      }
+      float up = top;
+#pragma unroll
+      for (int u = 0; u < U; ++u) up = fmaxf(up, st[u].x);
+      const float f0 = top == NEG_INF ? 0.f : ex2(top - up);
+      top = up;
+      sum *= f0;
+      x.x *= f0, x.y *= f0, x.z *= f0, x.w *= f0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float f = st[u].x == NEG_INF ? 0.f : ex2(st[u].x - top);
+        sum = fmaf(st[u].y, f, sum);
+        x.x = fmaf(y0[u].x, f, x.x), x.y = fmaf(y0[u].y, f, x.y), x.z = fmaf(y1[u].x, f, x.z), x.w = fmaf(y1[u].y, f, x.w);
+      }
+    }
+    const int row = s.rt * PAIR + r, token = a.by_group(row), hd = s.h * a.group + row - token * a.group;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint2 w;
+    w.x = pack_bf16x2(x.x * inv, x.y * inv);
+    w.y = pack_bf16x2(x.z * inv, x.w * inv);
+    *reinterpret_cast<uint2*>(a.O + (int64_t)hd * a.o_head + (int64_t)(s.q0 + token) * a.o_row + ch) = w;
+    if (lane == 0 && a.lse)
+      a.lse[(int64_t)hd * a.total_q + s.q0 + token] = sum == 0.f ? NEG_INF : (top + log2f(sum)) * (1.f / LOG2E);
   }
-  const int row = s.rt * PAIR + r, token = row / a.group, hd = s.h * a.group + row - token * a.group;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint2 w;
-  w.x = pack_bf16x2(x.x * inv, x.y * inv);
-  w.y = pack_bf16x2(x.z * inv, x.w * inv);
-  *reinterpret_cast<uint2*>(a.O + (int64_t)hd * a.o_head + (int64_t)(s.q0 + token) * a.o_row + ch) = w;
-  if (ch == 0 && a.lse)
-    a.lse[(int64_t)hd * a.total_q + s.q0 + token] = sum == 0.f ? NEG_INF : (top + log2f(sum)) * (1.f / LOG2E);
 }
 
 template <int NG>
@@ -834,13 +853,15 @@ cudaError_t launch(const AttendArgs& a, int dev, cudaStream_t st) {
   kv4_prompt_kernel<NG><<<grid, THREADS, S::CUM + (a.B + 1) * 4, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  kv4_prompt_join_kernel<<<dim3(grid, PAIR / JOIN_ROWS), JOIN_THREADS, (a.B + 1) * 4, st>>>(a, grid);
+  kv4_prompt_join_kernel<<<dim3(grid, PAIR / JOIN_ROWS), JOIN_THREADS, 0, st>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t kv4_prompt_partial_bytes() { return (size_t)KV4_MAX_CTAS * 2 * PAIR * PART * sizeof(float); }
+size_t kv4_prompt_partial_bytes() {
+  return (size_t)KV4_MAX_CTAS * (2 * PAIR * PART * sizeof(float) + sizeof(JoinInfo));
+}
 
 cudaError_t launch_kv4_prompt(const AttendArgs& a, int ng, int dev, cudaStream_t st) {
   return ng == 1 ? launch<1>(a, dev, st) : ng == 2 ? launch<2>(a, dev, st) : launch<4>(a, dev, st);
