@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv4_slots_kernel(const SlotArgs 
   const int64_t step = (int64_t)gridDim.x * SLOT_THREADS;
   for (int64_t t = (int64_t)blockIdx.x * SLOT_THREADS + threadIdx.x; t < total; t += step) {
     const int b = find_last(cum_new, a.B, (int32_t)t);
-    const int32_t have = kv[b] & 0x7fffffff, pos = (int32_t)((uint32_t)have + (uint32_t)(t - cum_new[b]));
+    // (a refused request's length may already be written back: as it was)
+    const int32_t have = kv[b] >= 0 ? kv[b] : a.kv_lens[b], pos = (int32_t)((uint32_t)have + (uint32_t)(t - cum_new[b]));
     int64_t slot = -1;
     if (served(b)) {
       const int32_t blk = pos >> P, held = (int32_t)(((int64_t)have + (1 << P) - 1) >> P);
@@ -491,8 +492,9 @@ msa_status msa_kv4_slots(const msa_kv4_cache* cache, const int32_t* kv_lens, con
   if (B && (!kv_lens || !new_lens || !kv_lens_out || (max_blocks && !block_table))) return MSA_ERR_INVALID_ARG;
   if (capacity && (!slots || !positions)) return MSA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(slots) & 7) return MSA_ERR_ALIGN;
-  // positions and page counts are 32-bit: a row holds fewer than 2^31 tokens
-  if (((int64_t)max_blocks << a.c.page_shift) > 0x7fffffff) return MSA_ERR_UNSUPPORTED;
+  if (!aligned4({kv_lens, new_lens, block_table, free_pages, n_free, kv_lens_out, n_free_out, cu_new, positions}))
+    return MSA_ERR_ALIGN;
+  if (((int64_t)max_blocks << a.c.page_shift) > KV4_MAX_TOKENS) return MSA_ERR_UNSUPPORTED;
   a.kv_lens = kv_lens, a.new_lens = new_lens, a.free_pages = free_pages, a.n_free = n_free;
   a.block_table = block_table, a.kv_out = kv_lens_out, a.n_free_out = n_free_out, a.cu_new = cu_new;
   a.positions = positions, a.slots = slots, a.table_stride = table_stride, a.capacity = capacity;
@@ -525,7 +527,8 @@ msa_status msa_kv4_release(const msa_kv4_cache* cache, const int32_t* ids, int32
   if (n > KV4_MAX_B) return MSA_ERR_UNSUPPORTED;
   if (table_stride < max_blocks) return MSA_ERR_SHAPE;
   if (n == 0) return MSA_OK;
-  if (!ids || !kv_lens || !block_table || !free_pages || !n_free) return MSA_ERR_INVALID_ARG;
+  if (!ids || !n_free || !free_pages || (B && (!kv_lens || (max_blocks && !block_table)))) return MSA_ERR_INVALID_ARG;
+  if (!aligned4({ids, kv_lens, block_table, free_pages, n_free})) return MSA_ERR_ALIGN;
   a.ids = ids, a.kv_lens = kv_lens, a.block_table = block_table, a.free_pages = free_pages, a.n_free = n_free;
   a.table_stride = table_stride, a.n = n, a.B = B, a.max_blocks = max_blocks;
   count_launches(1);

@@ -4,10 +4,13 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "msa_internal.h"
 
 namespace msa {
 
+constexpr int64_t KV4_MAX_TOKENS = 0x7fff0000;  // of a request
 constexpr int KV4_MAX_B = 2048;  // requests of one call: their prefix sums stay in shared memory
 
 struct Kv4View {
@@ -79,6 +82,12 @@ __device__ __forceinline__ bool request_lens(const AttendArgs& a, int b, int32_t
 // Many query rows (kv4_prompt.cu), at most KV4_PROMPT_MAX_B requests: two launches; `partial` holds kv4_prompt_partial_bytes().
 size_t kv4_prompt_partial_bytes();
 cudaError_t launch_kv4_prompt(const AttendArgs& a, int ng, int dev, cudaStream_t st);
+
+inline bool aligned4(std::initializer_list<const void*> pointers) {
+  for (const void* p : pointers)
+    if (reinterpret_cast<uintptr_t>(p) & 3) return false;
+  return true;
+}
 
 // Argument checks shared by the calls, and the view the kernels get.
 msa_status kv4_view(const msa_kv4_cache* c, Kv4View* v);

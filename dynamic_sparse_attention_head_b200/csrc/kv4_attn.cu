@@ -332,26 +332,28 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const __grid_cons
     const int row0 = s.rt * ROWS, rows = min(ROWS, s.n * a.group - row0);
     const int seen_first = s.kv - s.n + a.by_group(row0) + 1;
 
-    // ---- queries: operand B of S^T, column g = row, scaled by a power of two into fp16 ----
+    // ---- queries: operand B of S^T, column g = row, each row scaled by a power of two of its own into
+    // fp16 (a row of large or infinite channels leaves its neighbours as they are) ----
     uint32_t qf[NT][8][2];
     float qs[NG][NT][2];
     int lim[NT][2], token_of[NT][2];
-    float to_score;
+    float to_score[NT][2];  // of columns 2c, 2c + 1, as qs
     {
       uint4 raw[NT][4];
-      float top = 0.f;
+      float top[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int r = row0 + nt * 8 + g;
         const bool live = nt * 8 + g < rows;
         const int tok = live ? a.by_group(r) : 0, hd = live ? r - tok * a.group : 0;
         const __nv_bfloat16* q = a.Q + (int64_t)(s.h * a.group + hd) * a.q_head + (int64_t)(s.q0 + tok) * a.q_row;
+        top[nt] = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           raw[nt][i] = live ? *reinterpret_cast<const uint4*>(q + 32 * i + 8 * c) : make_uint4(0, 0, 0, 0);
           const uint32_t w[4] = {raw[nt][i].x, raw[nt][i].y, raw[nt][i].z, raw[nt][i].w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(bf_lo(w[k])), fabsf(bf_hi(w[k]))));
+          for (int k = 0; k < 4; ++k) top[nt] = fmaxf(top[nt], fmaxf(fabsf(bf_lo(w[k])), fabsf(bf_hi(w[k]))));
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -361,15 +363,18 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const __grid_cons
         }
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // 2^10 over the largest magnitude, rounded down to a power of two: exact but for elements
-      // 2^-24 of the largest and below
-      const int ex = (int)((__float_as_uint(top) >> 23) & 255);
-      const int up = max(-100, min(100, 136 - ex));
-      const float norm = __uint_as_float((uint32_t)(127 + up) << 23);
-      to_score = a.scale2 * __uint_as_float((uint32_t)(127 - up) << 23) * 16777216.f;
-#pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+        top[nt] = fmaxf(top[nt], __shfl_xor_sync(0xffffffffu, top[nt], 1));
+        top[nt] = fmaxf(top[nt], __shfl_xor_sync(0xffffffffu, top[nt], 2));
+        // 2^10 over the row's largest magnitude, rounded down to a power of two: exact but for elements
+        // 2^-24 of the largest and below.  Its reciprocal and the 2^24 of the codes come back with the
+        // softmax scale, in one product a score.
+        const int ex = (int)((__float_as_uint(top[nt]) >> 23) & 255);
+        const int up = max(-100, min(100, 136 - ex));
+        const float norm = __uint_as_float((uint32_t)(127 + up) << 23), norm24 = __uint_as_float((uint32_t)(103 + up) << 23);
+        const float back = a.scale2 * __uint_as_float((uint32_t)(127 - up) << 23) * 16777216.f;
+        to_score[nt][0] = __shfl_sync(0xffffffffu, back, 8 * c);
+        to_score[nt][1] = __shfl_sync(0xffffffffu, back, 8 * c + 4);
         float sum[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -390,8 +395,9 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const __grid_cons
           for (int i = gr * 4 / NG; i < (gr + 1) * 4 / NG; ++i) x += sum[i];
           x += __shfl_xor_sync(0xffffffffu, x, 1);
           x += __shfl_xor_sync(0xffffffffu, x, 2);
-          qs[gr][nt][0] = a.scale2 * __shfl_sync(0xffffffffu, x, 8 * c);
-          qs[gr][nt][1] = a.scale2 * __shfl_sync(0xffffffffu, x, 8 * c + 4);
+          x *= norm24;
+          qs[gr][nt][0] = __shfl_sync(0xffffffffu, x, 8 * c);
+          qs[gr][nt][1] = __shfl_sync(0xffffffffu, x, 8 * c + 4);
         }
       }
     }
@@ -466,10 +472,11 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const __grid_cons
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float x = -base[nt][e];
+              float x = 0.f;
 #pragma unroll
               for (int gr = 0; gr < NG; ++gr)
-                x = fmaf(acc[gr][nt][2 * r + e], bf_lo(ksw[gr]) * to_score, fmaf(bf_hi(ksw[gr]), qs[gr][nt][e], x));
+                x = fmaf(acc[gr][nt][2 * r + e], bf_lo(ksw[gr]), gr ? fmaf(bf_hi(ksw[gr]), qs[gr][nt][e], x) : bf_hi(ksw[gr]) * qs[gr][nt][e]);
+              x = fmaf(x, to_score[nt][e], -base[nt][e]);
               if (PARTIAL && (!shown || key >= lim[nt][e])) x = NEG_INF;
               sc[mt][nt][2 * r + e] = x;
               top[nt][e] = fmaxf(top[nt][e], x);
@@ -778,7 +785,13 @@ cudaError_t launch_rows(const AttendArgs& a, int max_q, int dev, cudaStream_t st
   return launch<NG, 2, 32, 8, 3>(a, dev, st);
 }
 
-constexpr int PROMPT_ROWS = 64;  // query rows of a KV head from which on the tensor-memory kernel is taken
+// Query rows of a KV head, of a request, from which on the tensor-memory kernel is taken.  It walks over 256
+// rows at a time at the cost of 128, the kernel here over 16: measured (28 / 4, 32 / 8 and 16 / 16 heads, 1, 8 and 32
+// requests of 32K, 8K and 2K tokens) they meet between 60 and 220 rows (8 x 8K tokens, 28 / 4 heads: 66.6 us here,
+// 78.2 there at 56 rows; 103 and 84 at 112).  Where the table's rows hold little, a walk ends before that cost
+// counts and the second launch of the other does: at 600 tokens they meet at 512 rows (57.5 and 57.9 us, 32 / 8
+// heads; 28.9 and 41.2 at 128).
+constexpr int PROMPT_ROWS = 96, PROMPT_ROWS_SHORT = 512, SHORT_TOKENS = 1024;
 constexpr size_t ARRIVALS_BYTES = 1024;
 constexpr size_t PARTIAL_BYTES = (size_t)KV4_MAX_CTAS * 2 * MAX_ROWS * PART * sizeof(float);
 static_assert(ARRIVALS_BYTES >= KV4_MAX_CTAS * 4, "a counter per CTA");
@@ -802,12 +815,13 @@ msa_status msa_kv4_attend(const msa_kv4_cache* cache, const void* Q, void* O, co
   AttendArgs a{};
   const msa_status st = kv4_view(cache, &a.c);
   if (st != MSA_OK) return st;
-  if (!strides || total_q < 0 || B < 0 || max_q < 0 || max_blocks < 0 || !(scale > 0.f) || scale > 3.4e38f)
+  if (!strides || total_q < 0 || B < 0 || max_q < 0 || max_blocks < 0 || !(scale > 0.f) || !isfinite(scale * LOG2E))
     return MSA_ERR_INVALID_ARG;
   if (Hq < 1 || Hq % cache->Hkv) return MSA_ERR_SHAPE;
   if (table_stride < max_blocks) return MSA_ERR_SHAPE;
   if (B > KV4_MAX_B || Hq > 65536) return MSA_ERR_UNSUPPORTED;
-  if (((int64_t)max_blocks << a.c.page_shift) > 0x7fffffff) return MSA_ERR_UNSUPPORTED;
+  // tokens are numbered in 32 bits, those of the tiles that a warp looks ahead to among them
+  if (((int64_t)max_blocks << a.c.page_shift) > KV4_MAX_TOKENS) return MSA_ERR_UNSUPPORTED;
   if ((int64_t)total_q * (Hq / cache->Hkv) > 0x7fffffff) return MSA_ERR_UNSUPPORTED;
   if (!ws) return MSA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(ws) % 256) return MSA_ERR_ALIGN;
@@ -815,6 +829,7 @@ msa_status msa_kv4_attend(const msa_kv4_cache* cache, const void* Q, void* O, co
   if (total_q == 0 || B == 0) return MSA_OK;
   if (!Q || !O || !kv_lens || !cu_q || (max_blocks && !block_table)) return MSA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(Q) | reinterpret_cast<uintptr_t>(O)) & 15) return MSA_ERR_ALIGN;
+  if (!aligned4({block_table, kv_lens, cu_q, lse})) return MSA_ERR_ALIGN;
   if (strides->q_head % 8 || strides->q_row % 8 || strides->o_head % 8 || strides->o_row % 8) return MSA_ERR_ALIGN;
   a.Q = static_cast<const __nv_bfloat16*>(Q);
   a.O = static_cast<__nv_bfloat16*>(O);
@@ -836,7 +851,8 @@ msa_status msa_kv4_attend(const msa_kv4_cache* cache, const void* Q, void* O, co
   if (cudaGetDevice(&dev) != cudaSuccess) return MSA_ERR_CUDA;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if ((int64_t)max_q * a.group >= PROMPT_ROWS && B <= KV4_PROMPT_MAX_B) e = launch_kv4_prompt(a, 128 / cache->group, dev, cs);
+  const int prompt_rows = ((int64_t)max_blocks << a.c.page_shift) < SHORT_TOKENS ? PROMPT_ROWS_SHORT : PROMPT_ROWS;
+  if ((int64_t)max_q * a.group >= prompt_rows && B <= KV4_PROMPT_MAX_B) e = launch_kv4_prompt(a, 128 / cache->group, dev, cs);
   else switch (cache->group) {
     case 128: e = launch_rows<1>(a, max_q, dev, cs); break;
     case 64: e = launch_rows<2>(a, max_q, dev, cs); break;

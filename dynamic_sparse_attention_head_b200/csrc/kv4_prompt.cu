@@ -27,6 +27,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kernels.h"
 #include "kv4.cuh"
@@ -246,6 +247,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
   typename S::Ctrl& ct = *reinterpret_cast<typename S::Ctrl*>(smem + S::CTRL);
   int32_t* cum = reinterpret_cast<int32_t*>(smem + S::CUM);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) join_info(a)[blockIdx.x].to = -1;
   if (smem_addr(smem) & 1023u) {  // swizzled tiles need a 1024-byte aligned base
     if (tid == 0) atomicOr(a.c.state, DEV_ERR_BOUNDS);
     return;
@@ -273,7 +275,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
   __syncthreads();
   const int64_t run = scan_units(a, cum, ct.sums, &ct.bad);
   if (blockIdx.x == 0 && tid == 0 && (ct.bad || run > 0x7fffffff)) atomicOr(a.c.state, DEV_ERR_BOUNDS);
-  if (tid == 0) join_info(a)[blockIdx.x].to = -1;
   if (run > 0x7fffffff) return;  // more units than the line has numbers for
   const int total = (int)run, active = active_ctas(total, gridDim.x);
   if ((int)blockIdx.x >= active || total == 0) return;
@@ -535,18 +536,27 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
           const float nb = m_used == NEG_INF ? 0.f : -m_used;
           const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(nb, nb);
           float2 rs2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          // ROUNDED: the fused product is exact where the maximum is rounded.  Above 2^24 the difference, half a
+          // last place of the maximum, would reach the exponent's range: scores are rounded first there.
+          const auto weights = [&](auto rounded) {
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint32_t pk[16];
+            for (int h = 0; h < 4; ++h) {
+              uint32_t pk[16];
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const float2 x = __ffma2_rn(make_float2(sv[32 * h + 2 * c], sv[32 * h + 2 * c + 1]), sc2, nb2);
-              const float2 e = make_float2(ex2(x.x), ex2(x.y));
-              rs2[c & 1] = __fadd2_rn(rs2[c & 1], e);
-              pk[c] = half2_bits(e.x, e.y);
+              for (int c = 0; c < 16; ++c) {
+                const float2 s2 = make_float2(sv[32 * h + 2 * c], sv[32 * h + 2 * c + 1]);
+                const float2 x = decltype(rounded)::value
+                                     ? make_float2(__fmul_rn(s2.x, sc) + nb, __fmul_rn(s2.y, sc) + nb)
+                                     : __ffma2_rn(s2, sc2, nb2);
+                const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                rs2[c & 1] = __fadd2_rn(rs2[c & 1], e);
+                pk[c] = half2_bits(e.x, e.y);
+              }
+              tmem_st16(s_own + 16 * h, pk);
             }
-            tmem_st16(s_own + 16 * h, pk);
-          }
+          };
+          if (__any_sync(0xffffffffu, fabsf(nb) > 0x1p24f)) weights(std::true_type{});
+          else weights(std::false_type{});
           l = l * alpha + ((rs2[0].x + rs2[1].x) + (rs2[0].y + rs2[1].y));
           tmem_wait_st();
           tc_fence_before();

@@ -407,10 +407,10 @@ size_t msa_kv4_page_bytes(int32_t page_tokens, int32_t group);
  * be its input), cu_new[B + 1] (running sum of new_lens), and for token t of cu_new[b] + i: slots[t]
  * (int64) and positions[t] = kv_lens[b] + i, for t below `capacity`; entries behind the last token
  * are left as they were.
- * A request that does not fit its row (or has a negative length, whose new tokens then count as
+ * A request that does not fit its row (or has a negative length; negative new tokens count as
  * none) gets no pages; from the first request on that the free pages do not suffice for, none
  * does: their slots are -1, kv_lens_out = kv_lens, and the error is recorded (msa_kv4_status).
- * B <= 2048.  Every pointer is a device pointer. */
+ * B <= 2048; a row holds at most 2^31 - 2^16 tokens.  Every pointer is a device pointer. */
 msa_status msa_kv4_slots(const msa_kv4_cache* cache, const int32_t* kv_lens, const int32_t* new_lens, int32_t B,
                          int32_t* block_table, int64_t table_stride, int32_t max_blocks, const int32_t* free_pages,
                          const int32_t* n_free, int32_t* kv_lens_out, int32_t* n_free_out, int32_t* cu_new,
@@ -439,12 +439,13 @@ msa_status msa_kv4_read(const msa_kv4_cache* cache, void* K, void* V, const msa_
 /* Attention over the cache: request b's query tokens are rows cu_q[b] .. cu_q[b + 1) of Q
  * [Hq][total_q][128] and the last of its kv_lens[b] cached tokens (append them first), so query i of
  * n sees the keys j <= kv_lens[b] - n + i:  O = softmax(Q K^T * scale) V over the values the cache
- * stands for (bf16), lse (optional, fp32 [Hq][total_q]) the natural-log normaliser.  A row that sees
+ * stands for (bf16; O may be Q itself, with its strides), lse (optional, fp32 [Hq][total_q]) the natural-log normaliser.  A row that sees
  * no key has O = 0 and lse = -inf.  Rows behind cu_q[B] are left as they were.  Query head h reads KV
  * head h / (Hq / Hkv).  Any number of query tokens per request (one each: decoding; a few: draft
  * verification; many: a prompt over a cached prefix); max_q, the most of any request, picks the
  * kernel's tile and nothing else.  Page numbers outside the cache hide their keys, lengths outside
- * the table row or Q are cut, and both are recorded as an error.  B <= 2048.
+ * the table row or Q are cut, and both are recorded as an error.  scale > 0.  B <= 2048, a row of the table
+ * holds at most 2^31 - 2^16 tokens.
  * ws: device, 256-byte aligned, msa_kv4_attend_workspace_bytes() bytes, zero-filled once by the
  * caller; every call leaves it ready for the next, of any shape.  Calls that may overlap on the GPU
  * need a workspace each.  Sums in fp32 and in a fixed order: the same inputs give the same bits. */

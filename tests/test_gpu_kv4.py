@@ -108,6 +108,11 @@ def test_slots_out_of_pages_and_rows():
     _slots([0, 4, 5], [20, 30, 2], 16, 4, 30, 10, True, cap=25)  # the map is too short: the rest is left out
 
 
+def test_slots_negative_lengths():
+    _slots([5, -3, 7], [2, 4, -6], 16, 4, 30, 10, True)
+    _slots([-1], [3], 16, 4, 30, 10, False)
+
+
 def test_slots_refuses_broken_free_count_on_the_device():
     cache = msa.KV4Cache.alloc(4, 1, 16, 64)
     nf, kv = _ints([9]), _ints([0])
@@ -304,31 +309,28 @@ SHAPES = [  # Hq, Hkv, page, group, kv lens, new tokens
     (16, 2, 64, 128, [5, 400], [40, 20]),              # more new tokens than cached ones
 ]
 
-PROMPT_ROWS = 64  # query rows of a KV head from which on the kernel for many rows is taken
+MANY = 1 << 20  # a hint that takes the kernel for many rows; 1: never does
 
 
-def _wide(Hq, Hkv, max_q):
-    return max_q * (Hq // Hkv) >= PROMPT_ROWS
-
-
+@pytest.mark.parametrize("max_q", [1, None, MANY])
 @pytest.mark.parametrize("Hq,Hkv,page,group,kv,new", SHAPES)
-def test_attention_against_64_bits(Hq, Hkv, page, group, kv, new):
+def test_attention_against_64_bits(Hq, Hkv, page, group, kv, new, max_q):
     rng = np.random.default_rng(sum(kv) + Hq)
     cache, table = _filled(rng, kv, Hkv, page, group)
     cu = np.concatenate(([0], np.cumsum(new))).tolist()
     Q = ko.bf16(rng.standard_normal((Hq, cu[-1], 128)) * 1.5)
-    ref = ko.attend(cache.pages.cpu().numpy(), page, group, Q, table, kv, cu, 0.1, wide=_wide(Hq, Hkv, max(new)))
-    o, L = _attend(cache, Q, table, kv, cu, 0.1, pad=3)
+    ref = ko.attend(cache.pages.cpu().numpy(), page, group, Q, table, kv, cu, 0.1, wide=max_q == MANY)
+    o, L = _attend(cache, Q, table, kv, cu, 0.1, pad=3, max_q=max_q)
     assert cache.device_status() == 0
     _compare(o, L, ref)
 
 
-@pytest.mark.parametrize("max_q", [0, 1, 100000])
+@pytest.mark.parametrize("max_q", [0, 1, 5, MANY])
 def test_attention_hint_only_picks_the_tile(max_q):
     rng = np.random.default_rng(2)
     cache, table = _filled(rng, [130, 50], 2, 64, 64)
     Q = ko.bf16(rng.standard_normal((8, 8, 128)))
-    ref = ko.attend(cache.pages.cpu().numpy(), 64, 64, Q, table, [130, 50], [0, 5, 8], 0.2, wide=_wide(8, 2, max_q))
+    ref = ko.attend(cache.pages.cpu().numpy(), 64, 64, Q, table, [130, 50], [0, 5, 8], 0.2, wide=max_q == MANY)
     o, L = _attend(cache, Q, table, [130, 50], [0, 5, 8], 0.2, max_q=max_q)
     _compare(o, L, ref)
 
@@ -409,17 +411,17 @@ def test_attention_over_long_contexts_split_over_the_gpu(Hq, Hkv, page, group, k
     assert int(ws[:1024].max()) == 0  # ready for the next call
 
 
-@pytest.mark.parametrize("n", [2, 20])
+@pytest.mark.parametrize("n,max_q", [(2, 2), (20, MANY)])
 @pytest.mark.parametrize("scale_v", [2.0 ** 60, 2.0 ** -60])
-def test_attention_scales_far_from_one(scale_v, n):
+def test_attention_scales_far_from_one(scale_v, n, max_q):
     rng = np.random.default_rng(11)
     cache, table = _filled(rng, [150], 1, 16, 64, scale_v=scale_v)
     Q = ko.bf16(rng.standard_normal((4, n, 128)) * 1e-3)
-    ref = ko.attend(cache.pages.cpu().numpy(), 16, 64, Q, table, [150], [0, n], 0.1, wide=_wide(4, 1, n))
-    _compare(*_attend(cache, Q, table, [150], [0, n], 0.1), ref)
+    ref = ko.attend(cache.pages.cpu().numpy(), 16, 64, Q, table, [150], [0, n], 0.1, wide=max_q == MANY)
+    _compare(*_attend(cache, Q, table, [150], [0, n], 0.1, max_q=max_q), ref)
 
 
-@pytest.mark.parametrize("max_q", [1, 100])
+@pytest.mark.parametrize("max_q", [1, MANY])
 def test_attention_sharp_rows_and_rising_scores(max_q):
     """Scores that rise along the keys move the running maximum again and again; the largest weigh all."""
     rng = np.random.default_rng(12)
@@ -432,11 +434,11 @@ def test_attention_sharp_rows_and_rising_scores(max_q):
     cache.append(_dev(K), _dev(V), _ints(np.arange(n), torch.int64))
     Q = np.zeros((3, 1, 128))
     Q[0, 0, 0], Q[1, 0, 0], Q[2, 0, 0] = 4.0, -4.0, 1e-3
-    ref = ko.attend(cache.pages.cpu().numpy(), page, group, Q, table, [n], [0, 1], 1.0, wide=_wide(3, 1, max_q))
+    ref = ko.attend(cache.pages.cpu().numpy(), page, group, Q, table, [n], [0, 1], 1.0, wide=max_q == MANY)
     _compare(*_attend(cache, Q, table, [n], [0, 1], 1.0, max_q=max_q), ref)
 
 
-@pytest.mark.parametrize("max_q", [4, 100])
+@pytest.mark.parametrize("max_q", [4, MANY])
 def test_attention_nan_keys_reach_only_the_rows_that_see_them(max_q):
     rng = np.random.default_rng(13)
     K, V = _rows_of(rng, 1, 40)
@@ -446,7 +448,7 @@ def test_attention_nan_keys_reach_only_the_rows_that_see_them(max_q):
     cache = _cache(3, 1, 16, 64)
     cache.append(_dev(K), _dev(V), torch.arange(40, device="cuda"))
     Q = ko.bf16(rng.standard_normal((2, 4, 128)))
-    ref = ko.attend(cache.pages.cpu().numpy(), 16, 64, Q[:, :2], np.arange(3)[None], [38], [0, 2], 0.1, wide=_wide(2, 1, max_q))
+    ref = ko.attend(cache.pages.cpu().numpy(), 16, 64, Q[:, :2], np.arange(3)[None], [38], [0, 2], 0.1, wide=max_q == MANY)
     o, L = _attend(cache, Q, np.arange(3)[None], [40], [0, 4], 0.1, max_q=max_q)
     _compare(o[:, :2], L[:, :2], ref)
     assert torch.isnan(o[:, 2:]).all() and torch.isnan(L[:, 2:]).all()
@@ -457,7 +459,7 @@ def test_attention_nan_keys_reach_only_the_rows_that_see_them(max_q):
     assert torch.isfinite(o[:, 3, :64]).all() and torch.isnan(o[:, 3, 64:]).all()
 
 
-@pytest.mark.parametrize("max_q", [1, 100])
+@pytest.mark.parametrize("max_q", [1, MANY])
 def test_attention_records_and_hides_what_is_out_of_bounds(max_q):
     rng = np.random.default_rng(14)
     cache, table = _filled(rng, [100, 60], 1, 16, 64, extra_blocks=1)
@@ -466,7 +468,7 @@ def test_attention_records_and_hides_what_is_out_of_bounds(max_q):
     broken = table.copy()
     broken[0, 3] = cache.n_pages      # behind the cache
     broken[0, 5] = -1
-    ref = ko.attend(host, 16, 64, Q, table, [100, 60], [0, 1, 2], 0.1, wide=_wide(2, 1, max_q), hidden=lambda b, j: b == 0 and j // 16 in (3, 5))
+    ref = ko.attend(host, 16, 64, Q, table, [100, 60], [0, 1, 2], 0.1, wide=max_q == MANY, hidden=lambda b, j: b == 0 and j // 16 in (3, 5))
     o, L = _attend(cache, Q, broken, [100, 60], [0, 1, 2], 0.1, max_q=max_q)
     assert cache.device_status() == 8 and cache.device_status() == 0
     _compare(o, L, ref)
@@ -475,7 +477,7 @@ def test_attention_records_and_hides_what_is_out_of_bounds(max_q):
     assert cache.device_status() == 8
     # rows 100 .. of request 0's last page were never written: NaN, so only request 1 can be compared
     assert torch.isnan(o[:, 0]).all()
-    one = ko.attend(host, 16, 64, Q[:, 1:], table[1:], [60], [0, 1], 0.1, wide=_wide(2, 1, max_q))
+    one = ko.attend(host, 16, 64, Q[:, 1:], table[1:], [60], [0, 1], 0.1, wide=max_q == MANY)
     _compare(o[:, 1:], L[:, 1:], one)
     # query offsets that run backwards or out of Q: those requests are left out
     o, L = _attend(cache, Q, table, [100, 60], [5, 1, 2], 0.1, max_q=max_q)
@@ -497,10 +499,10 @@ def test_attention_one_workspace_for_calls_of_different_shapes_and_graphs():
     qs, ql = _dev(small), _dev(large)
     tab, kv, cs, cl = _ints(table), _ints([900, 333]), _ints([0, 1, 2]), _ints([0, 40, 70])
     o_s, o_l = torch.zeros_like(qs), torch.zeros_like(ql)
-    cache.attend(ql, o_l, tab, kv, cl, 40, 0.1, ws)
+    cache.attend(ql, o_l, tab, kv, cl, MANY, 0.1, ws)
     first = o_l.clone()
     graphs = []
-    for q, o, cu, n in ((qs, o_s, cs, 1), (ql, o_l, cl, 40)):
+    for q, o, cu, n in ((qs, o_s, cs, 1), (ql, o_l, cl, MANY)):
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             cache.attend(q, o, tab, kv, cu, n, 0.1, ws)
@@ -520,6 +522,40 @@ def test_attention_one_workspace_for_calls_of_different_shapes_and_graphs():
     graphs[0].replay()
     ref = ko.attend(host, 64, 64, small, table, [800, 333], [0, 1, 2], 0.1)
     assert (np.abs(_host(o_s) - ref[0]) <= ref[2]).all() and not torch.equal(o, o_s)
+
+
+@pytest.mark.parametrize("max_q", [3, MANY])
+def test_attention_rows_of_any_size_side_by_side(max_q):
+    """Rows of one tile whose queries are 2^60 times the others', infinite or NaN: every finite row is its own."""
+    rng = np.random.default_rng(19)
+    cache, table = _filled(rng, [200], 1, 16, 64)
+    Q = ko.bf16(rng.standard_normal((4, 3, 128)))
+    Q[0, 1] *= 2.0 ** -60
+    ref = ko.attend(cache.pages.cpu().numpy(), 16, 64, Q, table, [200], [0, 3], 0.1, wide=max_q == MANY)
+    broken = Q.copy()
+    broken[1, 0, 5], broken[2, 1, 100], broken[3, 2, 0] = np.inf, np.nan, -np.inf
+    broken[0, 2] = ko.bf16(Q[0, 2] * 2.0 ** 60)
+    o, L = _attend(cache, broken, table, [200], [0, 3], 0.1, max_q=max_q)
+    for h, t in ((1, 0), (2, 1), (3, 2)):
+        assert torch.isnan(o[h, t]).all() and torch.isnan(L[h, t])
+        o[h, t], L[h, t] = 0.0, 0.0
+        ref[0][h, t] = ref[1][h, t] = 0.0
+    big = ko.attend(cache.pages.cpu().numpy(), 16, 64, broken[:1], table, [200], [0, 3], 0.1, wide=max_q == MANY)
+    for x, y in zip(ref, big):  # scores of 2^60 too
+        x[0, 2] = y[0, 2]
+    _compare(o, L, ref)
+
+
+@pytest.mark.parametrize("max_q", [1, MANY])
+def test_attention_in_place(max_q):
+    rng = np.random.default_rng(20)
+    cache, table = _filled(rng, [700, 90, 33], 2, 16, 64)
+    q = _dev(rng.standard_normal((8, 60, 128)))
+    args = (_ints(table), _ints([700, 90, 33]), _ints([0, 37, 59, 60]), max_q, 0.1, cache.alloc_workspace())
+    o = torch.zeros_like(q)
+    cache.attend(q, o, *args)
+    cache.attend(q, q, *args)
+    assert torch.equal(o, q)
 
 
 def test_two_attention_calls_at_once_with_a_workspace_each():

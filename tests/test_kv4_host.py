@@ -1,6 +1,8 @@
 """Host side of the operators around the layer: sizes, argument checks and refusals of the calls (made
 before any device access, so placeholder addresses do), and the tests' own 64-bit forms."""
+import copy
 import ctypes
+import pickle
 
 import numpy as np
 import pytest
@@ -77,6 +79,14 @@ def test_rope_description_checks():
             msa.Rope(**kw)
 
 
+def test_rope_copies_stand_alone():
+    rope = msa.Rope(sections=(16, 24, 24), scale=0.5)
+    for twin in (copy.deepcopy(rope), pickle.loads(pickle.dumps(rope))):
+        assert ctypes.addressof(twin._c) != ctypes.addressof(rope._c)
+        assert bytes(twin._c) == bytes(rope._c) and twin.n_axes == 3
+        assert not any(v == ctypes.addressof(rope._c) for v in vars(twin).values() if isinstance(v, int))
+
+
 def test_cache_argument_checks():
     bad = [(dict(pages=None), INVALID), (dict(state=None), INVALID), (dict(n_pages=0), INVALID),
            (dict(n_pages=1 << 31), INVALID), (dict(page_tokens=48), SHAPE), (dict(group=16), SHAPE), (dict(Hkv=0), SHAPE),
@@ -122,6 +132,11 @@ def test_slots_release_argument_checks():
         assert release(**kw) == INVALID, kw
     assert release(stride=7) == SHAPE and release(n=2049) == UNSUPPORTED
     assert release(n=0, ids=None) == 0
+    for kw in (dict(kv=FAKE + 2), dict(new=FAKE + 2), dict(table=FAKE + 1), dict(free=FAKE + 2), dict(nf=FAKE + 2),
+               dict(kvo=FAKE + 2), dict(nfo=FAKE + 2), dict(cu=FAKE + 2), dict(pos=FAKE + 2)):
+        assert slots(**kw) == ALIGN, kw
+    for kw in (dict(ids=FAKE + 2), dict(kv=FAKE + 2), dict(table=FAKE + 2), dict(free=FAKE + 2), dict(nf=FAKE + 2)):
+        assert release(**kw) == ALIGN, kw
 
 
 def test_attend_argument_checks():
@@ -141,6 +156,11 @@ def test_attend_argument_checks():
     assert call(wb=ws - 1) == WORKSPACE
     assert call(B=2049) == UNSUPPORTED and call(blocks=1 << 26, stride=1 << 26) == UNSUPPORTED
     assert call(T=1 << 30, Hq=16) == UNSUPPORTED
+    # 2^31 - 2^15 tokens a row: numbers that a warp looks ahead to would pass 32 bits
+    assert call(blocks=(1 << 31) - (1 << 15) >> 6, stride=1 << 26) == UNSUPPORTED
+    for kw in (dict(table=FAKE + 2), dict(kv=FAKE + 1), dict(cu=FAKE + 2), dict(lse=FAKE + 2)):
+        assert call(**kw) == ALIGN, kw
+    assert call(scale=3e38) == INVALID  # log2(e) of it is infinite
     assert call(T=0, Q=None, O=None) == 0 and call(B=0, kv=None, cu=None, table=None) == 0
 
 
