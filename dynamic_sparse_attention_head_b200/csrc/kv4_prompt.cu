@@ -20,8 +20,12 @@
 // come in equal folds on one line, of which every CTA takes an equal stretch.  A pair cut by a stretch's
 // border leaves fp32 rows in the workspace; a second small kernel joins them in a fixed order.
 //
-// Bound by the softmax warps' instruction issue, as the layer's own attention kernel; the tensor
-// pipe needs 2176 cycles per pair of tiles.
+// Measured (follow-up prompts of 601 and 316 tokens over 32768 and 10732 cached ones, 28 / 4 heads): 538 us, 610
+// TFLOP/s.  A pair of tiles takes 4700 to 6000 cycles.  The tensor pipe needs 2176 of them, the exponentials
+// 2048, shared memory about 2550 (147 KB of Q K operands, 64 KB of P V's, 115 KB around the widening); the
+// chain through them is what counts: widening 2700 (keys) and 1150 (values), products 1750 under that
+// contention, softmax 2440.  Moving the scales' share of the widening to a warp of its own shortened the first
+// but not the chain (573 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -82,7 +86,7 @@ struct PromptSmem {
     int32_t v_exp[4];               // exponent taken out of the values
     int32_t warp_exp[2][4];
     uint32_t tmem;
-    int32_t abort, bad, lock;
+    int32_t abort, bad;
   };
   static constexpr int CUM = CTRL + (sizeof(Ctrl) + 15) / 16 * 16;
 };
@@ -206,12 +210,6 @@ __device__ __forceinline__ JoinInfo* join_info(const AttendArgs& a) {
   return reinterpret_cast<JoinInfo*>(a.partial + (int64_t)KV4_MAX_CTAS * 2 * PAIR * PART);
 }
 
-__device__ __forceinline__ bool take_lock(int* lock, volatile int* abort) {
-  for (int i = 0; atomicCAS(lock, 0, 1) != 0; ++i)
-    if ((i & 63) == 63 && *abort) return false;
-  return true;
-}
-
 // 32-byte-swizzled operand of 16 columns: rows of 32 bytes, groups of 8 rows 256 bytes apart.
 __device__ __forceinline__ uint64_t smem_desc_sw32(uint32_t saddr) {
   uint64_t d = 0;
@@ -253,7 +251,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
     return;
   }
   if (tid == 0) {
-    ct.abort = ct.bad = ct.lock = 0;
+    ct.abort = ct.bad = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ct.raw_full[i], 1);
       mbar_init(&ct.raw_empty[i], 128);
@@ -344,8 +342,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
       }
     } else if ((warp & 1) && lane == 0) {
       // ---------------------------------------------------------------- MMA issuers: warp 1, 3
-      // As in the layer's attention kernel: QK(0), then groups [PV(j), QK(j + 1)] under a lock, so that the
-      // tensor pipe gets whole groups and the streams settle half a period apart.
+      // QK(0), then groups [PV(j), QK(j + 1)].  The two streams' groups may mix on the tensor pipe: Q K reads
+      // both operands from shared memory (128 bytes a cycle, all there is), P V one, and side by side they
+      // share it better than one after the other (538 us against 563 with the groups held apart by a lock).
       const int st = warp >> 1;
       constexpr uint32_t IDESC_QK = idesc_f16_f32(128, 128, 0, 0), IDESC_PV = idesc_f16_f32(128, 128, 0, 1);
       const uint32_t s_col = tmem + TM_STREAM * st;
@@ -378,16 +377,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
           }
           continue;
         }
-        ok = mbar_wait(&ct.q_full[st], done & 1, abort) && mbar_wait(&ct.k_full[kt & 1], (kt >> 1) & 1, abort) &&
-             take_lock(&ct.lock, abort);
+        ok = mbar_wait(&ct.q_full[st], done & 1, abort) && mbar_wait(&ct.k_full[kt & 1], (kt >> 1) & 1, abort);
         if (!ok) break;
         qk(kt);
-        atomicExch(&ct.lock, 0);
         for (int j = 0; j < n; ++j, ++kt, ++mine) {
           ok = (j > 0 || done == 0 || mbar_wait(&ct.o_free[st], (done - 1) & 1, abort)) &&
                mbar_wait(&ct.v_full, kt & 1, abort) && mbar_wait(&ct.p_full[st], mine & 1, abort) &&
-               (j + 1 == n || mbar_wait(&ct.k_full[(kt + 1) & 1], ((kt + 1) >> 1) & 1, abort)) &&
-               take_lock(&ct.lock, abort);
+               (j + 1 == n || mbar_wait(&ct.k_full[(kt + 1) & 1], ((kt + 1) >> 1) & 1, abort));
           if (!ok) break;
           tc_fence_after();
           uint32_t v_addr = smem_addr(smem + S::V);
@@ -398,7 +394,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
                     (j > 0 || kk > 0) ? 1u : 0u);
           umma_commit(&ct.v_empty);
           if (j + 1 < n) qk(kt + 1);
-          atomicExch(&ct.lock, 0);
         }
         if (!ok) break;
         umma_commit(&ct.o_full[st]);
