@@ -33,29 +33,36 @@ namespace {
 // ---------------------------------------------------------------------------------------
 constexpr int SLOT_THREADS = 512;
 
-// Inclusive scan of one value per thread over the block (every thread calls); `sums`: one per warp.
-__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* sums) {
+// Inclusive scans of N values per thread over the block of SLOT_THREADS (every thread calls), and their totals.
+// `sums`: [N][SLOT_THREADS / 32].
+template <int N>
+__device__ __forceinline__ void block_scan(int64_t (&x)[N], int64_t (&total)[N], int64_t* sums) {
+  constexpr int WARPS = SLOT_THREADS / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) sums[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    int64_t s = lane < (int)(blockDim.x >> 5) ? sums[lane] : 0;
+  for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
+    for (int k = 0; k < N; ++k) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x[k], o);
+      if (lane >= o) x[k] += y;
     }
-    sums[lane] = s;
-  }
+  if (lane == 31)
+#pragma unroll
+    for (int k = 0; k < N; ++k) sums[k * WARPS + warp] = x[k];
   __syncthreads();
-  if (warp) x += sums[warp - 1];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    // every warp adds up the warps before it, and all of them
+    int64_t s = lane < WARPS ? sums[k * WARPS + lane] : 0, before = lane < warp ? s : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    x[k] += before;
+    total[k] = s;
+  }
   __syncthreads();  // `sums` is free again
-  return x;
 }
 
 // Largest b in [0, n) with cum[b] <= x (cum ascending, cum[0] = 0).
@@ -89,23 +96,24 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv4_slots_kernel(const SlotArgs 
   int32_t* cum_new = sm;                      // [B + 1]
   int32_t* cum_page = cum_new + a.B + 1;      // [B + 1]: pages wanted by the requests before b
   int32_t* kv = cum_page + a.B + 1;           // [B]
-  __shared__ int64_t sums[32];
+  __shared__ int64_t sums[2 * SLOT_THREADS / 32];
   __shared__ int last, bad;
   const int P = a.c.page_shift;
-  if (threadIdx.x == 0) bad = 0;
-  __syncthreads();
+  // the first lengths are asked for together with the count
   int64_t n_free = *a.n_free;
-  if (n_free < 0 || n_free > a.c.n_pages) {
-    if (threadIdx.x == 0) bad = 1;
-    n_free = n_free < 0 ? 0 : a.c.n_pages;
-  }
+  int32_t next_have = (int)threadIdx.x < a.B ? a.kv_lens[threadIdx.x] : 0;
+  int32_t next_new = (int)threadIdx.x < a.B ? a.new_lens[threadIdx.x] : 0;
+  if (threadIdx.x == 0) bad = n_free < 0 || n_free > a.c.n_pages;
+  n_free = min(max(n_free, (int64_t)0), a.c.n_pages);
+  __syncthreads();
   int64_t run_new = 0, run_page = 0;
   for (int b0 = 0; b0 < a.B; b0 += SLOT_THREADS) {
     const int b = b0 + threadIdx.x;
     int64_t n = 0, pages = 0;
     if (b < a.B) {
-      const int64_t have = a.kv_lens[b];
-      n = a.new_lens[b];
+      const int64_t have = next_have;
+      n = next_new;
+      if (b + SLOT_THREADS < a.B) next_have = a.kv_lens[b + SLOT_THREADS], next_new = a.new_lens[b + SLOT_THREADS];
       if (have < 0 || n < 0) bad = 1;
       if (n < 0) n = 0;
       kv[b] = (int32_t)have;
@@ -123,26 +131,27 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv4_slots_kernel(const SlotArgs 
     }
     // a request that fits no row is marked by the sign of its length and wants no page
     const bool refused = pages < 0;
-    const int64_t cn = block_scan(n, sums) + run_new, cp = block_scan(refused ? 0 : pages, sums) + run_page;
+    int64_t x[2] = {n, refused ? 0 : pages}, all[2];
+    block_scan(x, all, sums);
+    const int64_t cn = x[0] + run_new, cp = x[1] + run_page;
     if (b < a.B) {
       if (cn > 0x7fffffff || cp > 0x7fffffff) bad = 1;
       cum_new[b + 1] = (int32_t)min(cn, (int64_t)0x7fffffff);
       cum_page[b + 1] = (int32_t)min(cp, (int64_t)0x7fffffff);
       if (refused) kv[b] = kv[b] | (int32_t)0x80000000;
     }
-    if (threadIdx.x == SLOT_THREADS - 1) sums[31] = cn, sums[30] = cp;
-    __syncthreads();
-    run_new = sums[31];
-    run_page = sums[30];
-    __syncthreads();
+    run_new += all[0];
+    run_page += all[1];
   }
-  if (threadIdx.x == 0) {
-    cum_new[0] = cum_page[0] = 0;
-    // this block has read every length: the last block to say so may overwrite them
-    __threadfence();
-    last = atomicAdd(a.c.state + 1, 1u) == gridDim.x - 1;
-  }
+  if (threadIdx.x == 0) cum_new[0] = cum_page[0] = 0;
   __syncthreads();
+  // this block has read every length: the last block to say so may overwrite them.  One thread asks, and
+  // the answer is waited for at the end
+  uint32_t before = 0;
+  if (gridDim.x > 1 && threadIdx.x == SLOT_THREADS - 1) {
+    __threadfence();
+    before = atomicAdd(a.c.state + 1, 1u);
+  }
   const auto served = [&](int b) { return kv[b] >= 0 && cum_page[b + 1] <= n_free; };
 
   const int64_t total = min((int64_t)cum_new[a.B], a.capacity);
@@ -170,6 +179,8 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv4_slots_kernel(const SlotArgs 
     const int32_t held = (int32_t)(((int64_t)kv[b] + (1 << P) - 1) >> P);
     a.block_table[b * a.table_stride + held + (int32_t)(k - cum_page[b])] = a.free_pages[n_free - 1 - k];
   }
+  if (threadIdx.x == SLOT_THREADS - 1) last = before == gridDim.x - 1;
+  __syncthreads();
   if (last) {
     int64_t taken = 0;
     for (int b = threadIdx.x; b < a.B; b += SLOT_THREADS) {
@@ -187,7 +198,7 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv4_slots_kernel(const SlotArgs 
       for (int w = 0; w < SLOT_THREADS / 32; ++w) taken = max(taken, sums[w]);
       a.cu_new[0] = 0;
       *a.n_free_out = (int32_t)(n_free - taken);
-      a.c.state[1] = 0;
+      if (gridDim.x > 1) a.c.state[1] = 0;
     }
   }
   __syncthreads();
@@ -207,7 +218,7 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv4_release_kernel(const Release
   extern __shared__ int32_t sm[];
   int32_t* ids = sm;            // [n]
   int32_t* cum = ids + a.n;     // [n + 1]
-  __shared__ int64_t sums[32];
+  __shared__ int64_t sums[SLOT_THREADS / 32];
   __shared__ int bad;
   if (threadIdx.x == 0) bad = 0;
   for (int i = threadIdx.x; i < a.n; i += SLOT_THREADS) ids[i] = a.ids[i];
@@ -233,12 +244,10 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv4_release_kernel(const Release
         pages = min(pages, (int64_t)a.max_blocks);
       }
     }
-    const int64_t c = block_scan(pages, sums) + run;
-    if (i < a.n) cum[i + 1] = (int32_t)min(c, (int64_t)0x7fffffff);
-    if (threadIdx.x == SLOT_THREADS - 1) sums[31] = c;
-    __syncthreads();
-    run = sums[31];
-    __syncthreads();
+    int64_t x[1] = {pages}, all[1];
+    block_scan(x, all, sums);
+    if (i < a.n) cum[i + 1] = (int32_t)min(x[0] + run, (int64_t)0x7fffffff);
+    run += all[0];
   }
   if (threadIdx.x == 0) cum[0] = 0;
   __syncthreads();

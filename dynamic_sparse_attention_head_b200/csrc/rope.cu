@@ -15,6 +15,7 @@
 // fp32, 471 us (issue-bound).
 #include <cuda_bf16.h>
 #include <math.h>
+#include <string.h>
 
 #include <algorithm>
 
@@ -213,6 +214,29 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) qk_norm_rope_kernel
   }
 }
 
+// The fraction of a turn per position, in [0, 1), as 64 bits (what rounds up to a turn wraps to 0).  A call does
+// this for every frequency, so those of a model are taken in integers: w = m 2^-s, and m / 2 pi has 117 bits, its
+// fraction behind the binary point to 2^-128 (in long double a decode step's call took 5.4 us of host time, more
+// than its kernel).
+uint64_t turn_of(double w) {
+  constexpr long double INV = 0.5L / 3.14159265358979323846264338327950288L;
+  constexpr uint64_t HI = 0x28be60db9391054aull, LO = 0x7f09d5f47d4d3770ull;  // 2^128 / 2 pi
+  uint64_t bits;
+  memcpy(&bits, &w, 8);
+  const int ex = (int)(bits >> 52 & 2047), s = 1075 - ex;
+  if (ex == 0 || s > 127) return 0;  // below 2^-75: no turn in 2^64 positions
+  if (s >= 43) {                     // below 2^10
+    const uint64_t m = (bits & 0xfffffffffffffull) | 0x10000000000000ull;
+    const unsigned __int128 p = (unsigned __int128)m * HI + (uint64_t)((unsigned __int128)m * LO >> 64);
+    const uint64_t turn = (uint64_t)((p + ((unsigned __int128)1 << (s - 1))) >> s);
+    return bits >> 63 ? 0 - turn : turn;
+  }
+  long double f = (long double)w * INV;
+  f -= floorl(f);
+  const long double u = floorl(f * 18446744073709551616.0L + 0.5L);
+  return u >= 18446744073709551616.0L ? 0 : (uint64_t)u;
+}
+
 }  // namespace
 }  // namespace msa
 
@@ -252,11 +276,7 @@ extern "C" msa_status msa_qk_norm_rope(const void* Q, const void* K, const msa_s
     if (!isfinite(rope->inv_freq[i])) return MSA_ERR_INVALID_ARG;
     while (i >= end) end += rope->sections[++x];
     a.axis[i] = (uint8_t)x;
-    // fraction of a turn per position, in [0, 1), as 64 bits (a value that rounds up to 1 wraps to 0)
-    long double f = (long double)rope->inv_freq[i] / (2.0L * 3.14159265358979323846264338327950288L);
-    f -= floorl(f);
-    const long double u = floorl(f * 18446744073709551616.0L + 0.5L);
-    a.turn[i] = u >= 18446744073709551616.0L ? 0 : (uint64_t)u;
+    a.turn[i] = turn_of(rope->inv_freq[i]);
   }
   a.Q = static_cast<const __nv_bfloat16*>(Q), a.K = static_cast<const __nv_bfloat16*>(K);
   a.Qo = static_cast<__nv_bfloat16*>(Qo), a.Ko = static_cast<__nv_bfloat16*>(Ko);

@@ -80,6 +80,16 @@ def test_slots_decode_batch(page, alias):
     _slots(kv, [1] * 700, page, 7, need + 800, 750, alias)
 
 
+@pytest.mark.parametrize("B,cap", [(1, None), (511, None), (512, None), (513, None), (300, 40), (64, 0)])
+@pytest.mark.parametrize("most", [1, 4, 5])
+def test_slots_of_a_few_tokens_each(B, cap, most):
+    rng = np.random.default_rng(B + most)
+    kv, new = rng.integers(0, 70, B).tolist(), rng.integers(0, most + 1, B).tolist()
+    new[-1] = most
+    _slots(kv, new, 16, 6, 4 * 600 + 600, 590, True, cap=cap)
+    _slots(kv, new, 16, 6, 4 * 600 + 600, 7, False, cap=cap)  # the free pages end somewhere in the batch
+
+
 @pytest.mark.parametrize("alias", [False, True])
 def test_slots_prompts_over_several_blocks(alias):
     _slots([0, 17, 0, 400], [30000, 1, 0, 20011], 16, 2000, 6000, 5000, alias)
