@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const __grid_cons
   Segment* segs = reinterpret_cast<Segment*>(smem + S::SEGS);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BARS);
   int32_t* cum = reinterpret_cast<int32_t*>(smem + S::CUM);
-  __shared__ int abort_flag, bad, last_of[2], line_total, line_shift;
+  __shared__ int abort_flag, bad, last_of[2], last_to[2], line_total, line_shift;
   // 1: has a head, 2: the head's segment ends in the stretch, 4: has a tail, 8: the head is in the workspace
   __shared__ uint8_t ends[W];
 
@@ -239,9 +239,13 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const __grid_cons
   // a CTA takes at least a unit per warp where there are that many
   const int active = min((int)gridDim.x, max(1, (total + W - 1) / W));
   if ((int)blockIdx.x >= active || total <= 0) return;
-  const auto edge = [&](int i) { return (int)((int64_t)total * i / active); };
+  // floor(total i / active) and, below, the i whose stretch holds unit t, in 32 bits: a 64-bit quotient takes
+  // several hundred cycles, and a short context's launch waits for four of them
+  const int each = total / active, rest = total - each * active;
+  const auto edge = [&](int i) { return each * i + rest * i / active; };
   const int t0 = edge(blockIdx.x), t1 = edge(blockIdx.x + 1);
-  const int w0 = t0 + (int)((int64_t)(t1 - t0) * warp / W), w1 = t0 + (int)((int64_t)(t1 - t0) * (warp + 1) / W);
+  const uint32_t stretch = t1 - t0;  // of a whole GPU's 2^31 units: times W it fits 32 bits
+  const int w0 = t0 + (int)(stretch * warp / W), w1 = t0 + (int)(stretch * (warp + 1) / W);
 
   const auto locate = [&](int t) { return segment_at<NT>(a, cum, unit_shift, t); };
   // keys that the last row of the segment's tile sees (none: <= 0)
@@ -661,7 +665,12 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const __grid_cons
 
   // ---- segments over several warps: a chain is the tail (or the CTA's head) and the heads after it ----
   const auto part = [&](int i, int which) { return a.partial + (2 * (int64_t)i + which) * MAX_ROWS * PART; };
-  const auto owner = [&](int t) { return (int)((((int64_t)t + 1) * active - 1) / total); };
+  const auto owner = [&](int t) {
+    int i = min((int)__fdividef((float)t * (float)active, (float)total), active - 1);  // or next to it
+    while (edge(i) > t) --i;
+    while (edge(i + 1) <= t) ++i;
+    return i;
+  };
   uint32_t crosses = 0;  // bit 0: the CTA's head, bit 1: its tail, in the workspace
   Segment cross_seg[2];
   uint32_t has_head = 0, stops_in = 0, has_tail = 0, in_ws = 0;  // a bit per warp
@@ -673,7 +682,7 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const __grid_cons
     in_ws = __ballot_sync(0xffffffffu, e & 8);
   }
   int lead = 0;  // the first warp with a stretch
-  while ((int64_t)(t1 - t0) * (lead + 1) / W == 0) ++lead;
+  while (stretch * (lead + 1) / W == 0) ++lead;
 #pragma unroll 1
   for (uint32_t starts = has_tail << 1 | (has_head >> lead & 1); starts; starts &= starts - 1) {
     const int first = __ffs(starts) - 2;  // -1: the CTA's head
@@ -721,41 +730,46 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const __grid_cons
 
   // ---- segments over several CTAs: joined by the one that arrives last ----
   if (crosses) {
-    __threadfence();
-    __syncthreads();
+    int from = 0, to = 0;  // of thread w's crossing segment
     if (tid < 2 && (crosses >> tid & 1)) {
       const Segment& s = cross_seg[tid];
-      const int from = owner(s.first), to = owner(s.first + s.count - 1);
-      last_of[tid] = atomicAdd(a.arrivals + from, 1u) == (uint32_t)(to - from);
-      if (last_of[tid]) a.arrivals[from] = 0;  // ready for the next launch
-      __threadfence();
+      from = owner(s.first), to = owner(s.first + s.count - 1);
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid < 2) {
+      last_of[tid] = -1;
+      if (crosses >> tid & 1) {
+        const bool last = atomicAdd(a.arrivals + from, 1u) == (uint32_t)(to - from);
+        if (last) a.arrivals[from] = 0;  // ready for the next launch
+        if (last) last_of[tid] = from, last_to[tid] = to;
+        __threadfence();
+      }
     }
     __syncthreads();
 #pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-      if (!(crosses >> which & 1) || !last_of[which]) continue;
+    for (int i = tid; i < 2 * ROWS * (HD / 4); i += THREADS) {  // the rows of both
+      const int which = i / (ROWS * (HD / 4)), r = i / (HD / 4) % ROWS, ch = (i % (HD / 4)) * 4;
+      const int from = last_of[which], to = last_to[which];
+      if (from < 0) continue;
       const Segment s = cross_seg[which];
-      const int from = owner(s.first), to = owner(s.first + s.count - 1);
-      const int rows = min(ROWS, s.n * a.group - s.rt * ROWS);
-      for (int i = tid; i < rows * (HD / 4); i += THREADS) {
-        const int r = i / (HD / 4), ch = (i % (HD / 4)) * 4;
-        float top = NEG_INF, sum = 0.f;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int U = 8;  // partial results on their way together
-        for (int k0 = from; k0 <= to; k0 += U) {
-          float2 st[U];
-          float4 y[U];
+      if (r >= s.n * a.group - s.rt * ROWS) continue;
+      float top = NEG_INF, sum = 0.f;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      constexpr int U = 8;  // partial results on their way together
+      for (int k0 = from; k0 <= to; k0 += U) {
+        float2 st[U];
+        float4 y[U];
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const float* p = part(min(k0 + u, to), k0 + u == from);
-            st[u] = __ldcg(reinterpret_cast<const float2*>(p + MAX_ROWS * HD + 2 * r));
-            y[u] = __ldcg(reinterpret_cast<const float4*>(p + r * HD + ch));
-            if (k0 + u > to) st[u] = make_float2(NEG_INF, 0.f), y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-          }
-          add_parts(top, sum, x, st, y);
+        for (int u = 0; u < U; ++u) {
+          const float* p = part(min(k0 + u, to), k0 + u == from);
+          st[u] = __ldcg(reinterpret_cast<const float2*>(p + MAX_ROWS * HD + 2 * r));
+          y[u] = __ldcg(reinterpret_cast<const float4*>(p + r * HD + ch));
+          if (k0 + u > to) st[u] = make_float2(NEG_INF, 0.f), y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        write_row(s, s.rt * ROWS + r, a.by_group(s.rt * ROWS + r), ch, x, top, sum);
+        add_parts(top, sum, x, st, y);
       }
+      write_row(s, s.rt * ROWS + r, a.by_group(s.rt * ROWS + r), ch, x, top, sum);
     }
   }
   if (tid == 0) {
