@@ -60,23 +60,19 @@ struct AttendArgs {
 
 // A request's first query row, new tokens and cached tokens, cut to what Q and the table row hold;
 // false: something was cut.
+__device__ __forceinline__ bool cut_lens(const AttendArgs& a, int32_t q0, int32_t q1, int32_t& n, int32_t& kv) {
+  const bool good = q0 >= 0 && q1 >= q0 && q1 <= a.total_q;
+  n = good ? q1 - q0 : 0;
+  const int32_t most = (int32_t)((int64_t)a.max_blocks << a.c.page_shift);
+  const bool fits = kv >= 0 && kv <= most;
+  kv = min(max(kv, 0), most);
+  return good && fits;
+}
 __device__ __forceinline__ bool request_lens(const AttendArgs& a, int b, int32_t& q0, int32_t& n, int32_t& kv) {
-  bool ok = true;
   q0 = a.cu_q[b];
   const int32_t q1 = a.cu_q[b + 1];
-  if (q0 < 0 || q1 < q0 || q1 > a.total_q) {
-    ok = false;
-    n = 0;
-  } else {
-    n = q1 - q0;
-  }
   kv = a.kv_lens[b];
-  const int64_t most = (int64_t)a.max_blocks << a.c.page_shift;
-  if (kv < 0 || kv > most) {
-    ok = false;
-    kv = kv < 0 ? 0 : (int32_t)most;
-  }
-  return ok;
+  return cut_lens(a, q0, q1, n, kv);
 }
 
 // Many query rows (kv4_prompt.cu), at most KV4_PROMPT_MAX_B requests: two launches; `partial` holds kv4_prompt_partial_bytes().

@@ -200,17 +200,27 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const __grid_cons
   // contexts then spread over more warps.
   if (warp == 0) {
     uint32_t cut = 0;
-    uint64_t blocks = 0;  // of 16 keys
+    uint32_t blocks = 0;  // of 16 keys; of a lane at most 2^24, far above what is asked below
+    constexpr int U = 4;  // requests of a lane on their way together
 #pragma unroll 1
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      int32_t q0, n = 0, kv = 0;
-      if (b0 + lane < a.B && !request_lens(a, b0 + lane, q0, n, kv)) cut = 1;
-      blocks += (uint64_t)row_tiles<NT>(n, a.group) * a.c.Hkv * ((kv + 15) >> 4);
-    }
+    for (int b0 = 0; b0 < a.B; b0 += 32 * U) {
+      int32_t q0[U], q1[U], kv[U];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) blocks += __shfl_xor_sync(0xffffffffu, blocks, o);
+      for (int u = 0; u < U; ++u) {
+        const int b = min(b0 + 32 * u + lane, a.B - 1);
+        q0[u] = a.cu_q[b], q1[u] = a.cu_q[b + 1], kv[u] = a.kv_lens[b];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        int32_t n;
+        if (!cut_lens(a, q0[u], q1[u], n, kv[u])) cut = 1;
+        const uint64_t x = (uint64_t)row_tiles<NT>(n, a.group) * a.c.Hkv * ((kv[u] + 15) >> 4);
+        if (b0 + 32 * u + lane < a.B) blocks = (uint32_t)min((uint64_t)blocks + x, (uint64_t)1 << 24);
+      }
+    }
+    blocks = __reduce_add_sync(0xffffffffu, blocks);
     cut = __any_sync(0xffffffffu, cut);
-    const int shift = blocks < (uint64_t)gridDim.x * W * (TK / 16) ? 4 : (TK == 64 ? 6 : 5);
+    const int shift = blocks < gridDim.x * W * (TK / 16) ? 4 : (TK == 64 ? 6 : 5);
     uint64_t run = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < a.B; b0 += 32) {
