@@ -815,11 +815,11 @@ cudaError_t launch_rows(const AttendArgs& a, int max_q, int dev, cudaStream_t st
 
 // Query rows of a KV head, of a request, from which on the tensor-memory kernel is taken.  It walks over 256
 // rows at a time at the cost of 128, the kernel here over 16: measured (28 / 4, 32 / 8 and 16 / 16 heads, 1, 8 and 32
-// requests of 32K, 8K and 2K tokens) they meet between 60 and 220 rows (8 x 8K tokens, 28 / 4 heads: 66.6 us here,
-// 78.2 there at 56 rows; 103 and 84 at 112).  Where the table's rows hold little, a walk ends before that cost
-// counts and the second launch of the other does: at 600 tokens they meet at 512 rows (57.5 and 57.9 us, 32 / 8
-// heads; 28.9 and 41.2 at 128).
-constexpr int PROMPT_ROWS = 96, PROMPT_ROWS_SHORT = 512, SHORT_TOKENS = 1024;
+// requests of 32K, 8K and 2K tokens) they meet between 60 and 96 rows (8 x 8K tokens, 28 / 4 heads: 65.9 us here, 73.8
+// there at 56 rows, 90.4 and 76.2 at 84; 32 / 8 heads: 105 and 115.5 at 64, 147 and 117 at 96).  Where the table's
+// rows hold little, a walk ends before that cost counts and the second launch of the other does: at 600 tokens, 32 / 8
+// heads, 29.7 and 37.1 us at 128 rows, 59.3 and 60.9 at 512.
+constexpr int PROMPT_ROWS = 80, PROMPT_ROWS_SHORT = 512, SHORT_TOKENS = 1024;
 constexpr size_t ARRIVALS_BYTES = 1024;
 constexpr size_t PARTIAL_BYTES = (size_t)KV4_MAX_CTAS * 2 * MAX_ROWS * PART * sizeof(float);
 static_assert(ARRIVALS_BYTES >= KV4_MAX_CTAS * 4, "a counter per CTA");
