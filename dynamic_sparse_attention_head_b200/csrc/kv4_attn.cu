@@ -26,8 +26,8 @@
 // bandwidth.
 //
 // Floor for long contexts: HBM, 2 (64 + 4 NG) bytes per key and KV head.  Measured: 64 requests of up to 16384
-// tokens, 32 / 8 heads, groups of 128: 125 us, 4.47 TB/s (a copy: 6.44); one token over 1048576, 28 / 4 heads,
-// groups of 64: 135 us, the same rate; 4 requests of up to 700 tokens: 13.7 us.  Bound by the issue of 12 warps an SM (57 to
+// tokens, 32 / 8 heads, groups of 128: 118 to 125 us, 4.6 TB/s (a copy: 6.44); one token over 1048576, 28 / 4 heads,
+// groups of 64: 129 to 135 us, the same rate; 4 requests of up to 700 tokens: 12.3 us.  Bound by the issue of 12 warps an SM (57 to
 // 60 %, ALU 56 %: 259 instructions per 16 keys, half of them to take the codes apart) and, for 11 % of the
 // time, by the start and the joins.
 #include <cuda_bf16.h>
