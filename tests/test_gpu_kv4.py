@@ -534,6 +534,25 @@ def test_attention_one_workspace_for_calls_of_different_shapes_and_graphs():
     assert (np.abs(_host(o_s) - ref[0]) <= ref[2]).all() and not torch.equal(o, o_s)
 
 
+@pytest.mark.parametrize("B,max_q,wide", [(2048, 1, False), (1025, MANY, False), (1024, MANY, True)])
+def test_attention_most_requests(B, max_q, wide):
+    """The most requests of a call, and of the kernel for many rows (above it the other one serves)."""
+    rng = np.random.default_rng(B)
+    kv = rng.integers(0, 12, B)
+    K, V = _rows_of(rng, 1, int(kv.sum()))
+    cache = _cache(B, 1, 16, 128)
+    table = rng.permutation(B)[:, None]
+    sl = np.concatenate([table[b, 0] * 16 + np.arange(k) for b, k in enumerate(kv)])
+    cache.append(_dev(K), _dev(V), _ints(sl, torch.int64))
+    new = rng.integers(0, 3, B)
+    cu = np.concatenate(([0], np.cumsum(new))).tolist()
+    Q = ko.bf16(rng.standard_normal((2, cu[-1], 128)))
+    ref = ko.attend(cache.pages.cpu().numpy(), 16, 128, Q, table, kv.tolist(), cu, 0.1, wide=wide)
+    o, L = _attend(cache, Q, table, kv, cu, 0.1, max_q=max_q, pad=2)
+    assert cache.device_status() == 0
+    _compare(o, L, ref)
+
+
 @pytest.mark.parametrize("max_q", [3, MANY])
 def test_attention_rows_of_any_size_side_by_side(max_q):
     """Rows of one tile whose queries are 2^60 times the others', infinite or NaN: every finite row is its own."""
