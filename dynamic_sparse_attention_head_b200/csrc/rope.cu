@@ -252,7 +252,7 @@ extern "C" msa_status msa_qk_norm_rope(const void* Q, const void* K, const msa_s
   if (rope->n_axes < 1 || rope->n_axes > 4) return MSA_ERR_INVALID_ARG;
   if (T == 0 || Hq + (int64_t)Hkv == 0) return MSA_OK;
   if ((Hq && (!Q || !Qo)) || (Hkv && (!K || !Ko)) || (rope->dim && !positions)) return MSA_ERR_INVALID_ARG;
-  if (rope->dim && rope->n_axes > 1 && pos_stride < T) return MSA_ERR_SHAPE;
+  if (rope->dim && rope->n_axes > 1 && pos_stride < T && pos_stride != 0) return MSA_ERR_SHAPE;
   // rows are 128 contiguous elements and heads at most 65536; the token count keeps the grid in range
   if (Hq > 65536 || Hkv > 65536 || T > (int64_t(1) << 31)) return MSA_ERR_UNSUPPORTED;
   const auto misaligned = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; };

@@ -343,8 +343,8 @@ msa_status msa_vslash_estimate_static(const void* Q, const void* K, int64_t L, i
  * f = position * inv_freq[i], pairs (i, i + dim / 2) (RoFormer; half-split, as the workload
  * generator's rotary inputs) or, interleaved, (2 i, 2 i + 1).  Channels from `dim` on are passed
  * on unrotated and unscaled.  fp32 arithmetic, one rounding to bf16; the angle is exact modulo
- * one turn for every int32 position (negative ones too).
- *  - positions: device int32 [n_axes][pos_stride >= T]; frequency i uses axis a of the sections[a]
+ * one turn for every int32 position (negative ones too) and every frequency below 2^10.
+ *  - positions: device int32 [n_axes][pos_stride >= T] (0: one row for all axes); frequency i uses axis a of the sections[a]
  *    frequencies it falls in (time / height / width positions of video tokens; one axis: sections
  *    is ignored).
  *  - in / out strides: element strides, as for Q and K of the layer calls (q_head, q_row, k_head,

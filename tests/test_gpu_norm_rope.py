@@ -102,6 +102,26 @@ def test_given_frequencies_and_far_positions():
     _check(_host(o), x, pos, (128, inv, [0] * 64, False, 1.0), None)
 
 
+def test_frequencies_of_any_size():
+    """Above 2^10 a frequency is held to 2^-53 turns (long double), below 2^-75 it is no turn at all."""
+    rng = np.random.default_rng(9)
+    inv = [1023.99, 1024.0, -1024.5, 2e5, -6.5, 6.283185307179586, 1e-22, -1e-30, 5e-324, 2.0 ** -1022] + [0.1 * i for i in range(54)]
+    pos = np.array([[0, 1, -1, 7, -100, 100]], np.int32)
+    q = _dev(ko.bf16(rng.standard_normal((2, 6, 128))))
+    o, k = torch.empty_like(q), torch.empty_like(q[:1])
+    msa.qk_norm_rope(q, q[:1], o, k, torch.from_numpy(pos).cuda(), msa.Rope(inv_freq=inv))
+    _check(_host(o), _host(q), pos, (128, inv, [0] * 64, False, 1.0), None)
+
+
+def test_positions_of_text_shared_by_the_axes():
+    x = torch.randn(3, 17, 128, device="cuda").to(torch.bfloat16)
+    pos, rope = torch.arange(100, 117, dtype=torch.int32, device="cuda"), msa.Rope(sections=(16, 24, 24))
+    one, three = torch.empty_like(x), torch.empty_like(x)
+    msa.qk_norm_rope(x[:2], x[2:], one[:2], one[2:], pos.expand(3, 17), rope)
+    msa.qk_norm_rope(x[:2], x[2:], three[:2], three[2:], pos.repeat(3, 1), rope)
+    assert torch.equal(one, three)
+
+
 def test_zero_rows_and_large_values():
     q = torch.zeros(1, 3, 128, dtype=torch.bfloat16, device="cuda")
     q[0, 1] = 2.0 ** 50
