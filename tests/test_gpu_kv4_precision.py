@@ -1,0 +1,103 @@
+"""Attention over the 4-bit cache where few of the keys, or few of the values, outweigh the others: both kernels
+against 64 bits, with bounds relative to the magnitudes that a row itself weighs."""
+import numpy as np
+import pytest
+
+import kv4_oracle as ko
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+import dynamic_sparse_attention_head_b200 as msa  # noqa: E402
+
+I32 = torch.int32
+MANY = 1 << 20  # a hint that takes the kernel for many rows; 1: the one for few
+
+
+def _bf16(x):
+    return torch.as_tensor(x, dtype=torch.float32).to(torch.bfloat16).cuda()
+
+
+def _filled(K, V, page, group):
+    """A cache of one request whose pages lie in another order, and its table."""
+    Hkv, n = K.shape[:2]
+    pages = -(-n // page)
+    cache = msa.KV4Cache.alloc(pages + 2, Hkv, page, group)
+    cache.pages.fill_(0xFF)  # NaN scales until a row is written
+    table = torch.randperm(pages + 2, generator=torch.Generator().manual_seed(n))[:pages].cuda()
+    j = torch.arange(n, device="cuda")
+    cache.append(K, V, table[j // page] * page + j % page)
+    return cache, table.to(I32)[None]
+
+
+def _values(x, group):
+    """What the cache stands for, in 64 bits, from the format's definition: values, minima and steps a channel."""
+    code, step, lo = ko.quantise(x.double().cpu().numpy(), group)
+    step, lo = (np.repeat(a, group, -1) for a in (step, lo))
+    return [torch.from_numpy(a).cuda() for a in (lo + code * step, lo, step)]
+
+
+def _compare(cache, table, K, V, Q, scale, max_q, v_error, weight_error, B=200):
+    """K, V [1, kv, 128], Q [H, n, 128]; the last n keys are the queries' own.  B requests hold the same keys and ask the
+    same: with more of them than SMs a CTA walks over whole contexts, and what it sums up is not cut into short pieces.  What a kernel may be off by, with p the
+    weights and m the largest of them (the sums are over a row's keys):
+      scores: ko.tolerance's bound of fp32 sums (136 of them, 2^-24 each), times the largest sum of magnitudes, and for
+        the many-row kernel 2^-16 of the largest step per channel (fp16's subnormals): a relative error of every weight,
+        twice (numerator and denominator), with the exponential's 2^-21 and the sums' n / 2 * 2^-24;
+      weights: in fp16, 2^-11 relative and at least weight_error of m, times the largest magnitude of a value;
+      values: v_error[j], of every value of key j, and 2^-11 relative;
+      O: rounded to bf16, 2^-8."""
+    kv, n = K.shape[1], Q.shape[1]
+    (k, kl, ks), (v, vl, vs) = (_values(x, cache.group) for x in (K, V))
+    q = Q.double()
+    s = q @ k[0].T * scale
+    see = torch.arange(kv, device="cuda")[None] <= kv - n + torch.arange(n, device="cuda")[:, None]
+    s = s.masked_fill(~see, float("-inf"))
+    p = torch.softmax(s, -1)
+    reach = (q.abs() @ (kl.abs() + 15 * ks)[0].T).amax(-1, keepdim=True) * scale
+    if max_q == MANY:
+        reach = reach + ks.max() * q.abs().sum(-1, keepdim=True) * scale
+    ds = reach * 2.0 ** -16 + 2.0 ** -21 + (kv / 2 + 32) * 2.0 ** -24
+    mag = v.abs()[0] if max_q == MANY else ((vl + 8 * vs).abs() + 8 * vs)[0]  # few rows: codes less 8 beside lo + 8 step
+    O = p @ v[0]
+    # the largest weight is at least 1 / (weights' sum): p's own scale
+    bound = O.abs() * 2.0 ** -8 + (p @ mag) * (2.0 ** -10 + 2 * ds) + (p @ v_error)[..., None] + \
+        kv * weight_error * p.amax(-1, keepdim=True) * mag.max()
+    qs = Q.repeat(1, B, 1)
+    o, lse = torch.zeros_like(qs), torch.zeros(qs.shape[:2], device="cuda")
+    cache.attend(qs, o, table.repeat(B, 1), torch.full((B,), kv, dtype=I32, device="cuda"),
+                 torch.arange(0, B * n + 1, n, dtype=I32, device="cuda"), max_q, scale, cache.alloc_workspace(), lse=lse)
+    assert cache.device_status() == 0
+    O, bound, ds = O.repeat(1, B, 1), bound.repeat(1, B, 1), ds.repeat(1, B, 1)
+    err = (o.double() - O).abs()
+    assert (err <= bound).all(), f"{float((err / bound).max()):.2f} of the bound, off by {float(err.norm() / O.norm()):.2e}"
+    ref = torch.logsumexp(s, -1).repeat(1, B)
+    assert ((lse.double() - ref).abs() <= ds[..., 0] + 2.0 ** -21 * ref.abs().clamp(min=1)).all()
+    return o, O
+
+
+@pytest.mark.parametrize("max_q", [1, MANY])
+@pytest.mark.parametrize("kv,gap,at", [(32768, 17.0, 0), (32768, 18.0, 0), (100003, 18.0, 0), (40000, 17.5, 30011)])
+def test_keys_far_below_a_sink_still_weigh(kv, gap, at, max_q):
+    """One key whose value is zero lies `gap` above the scores of all others, which are N(0, 1): what they add up to is
+    the whole of O, though each of them weighs 2^-25 of the largest and less.  Weights keep 2^-32 of the largest: fp16's
+    smallest step is 2^-24, half of it is lost, and the largest weight is 2^7 (in the few-row kernel the factor is the
+    values' step, within 2 of its power of two).  The values are of one size, 2^-18 of the largest at most lost."""
+    g = torch.Generator(device="cuda").manual_seed(kv)
+    q = torch.randn(128, generator=g, device="cuda")
+    Q = q[None, None].expand(2, 5, 128).to(torch.bfloat16).contiguous()
+    K = torch.randn(1, kv, 128, generator=g, device="cuda")
+    V = 1 + 0.5 * torch.randn(1, kv, 128, generator=g, device="cuda")
+    scale = float(1 / q.norm())
+    K[0, at] = Q[0, 0].float() * (gap / (scale * float((Q[0, 0].float() * q).sum())))
+    V[0, at] = 0
+    K, V = K.to(torch.bfloat16), V.to(torch.bfloat16)
+    cache, table = _filled(K, V, 64, 64)
+    lost = torch.full((kv,), 2.0 ** -18 * float(V.abs().max()), dtype=torch.float64, device="cuda")
+    lost[at] = 0  # zero is exact
+    o, O = _compare(cache, table, K, V, Q, scale, max_q, lost, 2.0 ** -32 if max_q == MANY else 2.0 ** -31)
+    # the roundings of 32768 weights and more average out: of the norm, O's own is left
+    assert float((o.double() - O).norm() / O.norm()) < 2.0 ** -8 + 2.0 ** -10
