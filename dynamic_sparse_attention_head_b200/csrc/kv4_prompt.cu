@@ -6,7 +6,7 @@
 // four warps turn them into fp16 operands in 128-byte-swizzled shared memory, the codes entering as
 // fp16 subnormals (a mask and one product a pair); two warps issue the products (M = N = 128); two
 // warpgroups hold a query row per thread: maximum, exponentials and sums in fp32, O rescaled only
-// when the maximum grows by 2^8 or the values' power of two grows.
+// when the maximum grows by 2^8 or the values' power of two changes.
 //
 // Scores keep fp32's precision: the operands are exact.  A code less 8 has 3 bits (or is 8, a power of
 // two) and a step has 8, so (code - 8) * step fits fp16's 11 bits; what is left, lo + 8 step per group,
@@ -63,6 +63,12 @@ constexpr int NAN_RING = 4;
 // go missing: O of 32768 of them was off by 1.7 % of its norm, at 18 nats by 14 %.
 constexpr int W_EXP = 7;
 constexpr int DEQ_UNROLL = 2;
+// A power of two is taken out of each tile's values, so that the largest lies in [2^-7, 2^-6); fp16 then holds
+// 2^-18 of it.  It is the one of the tile before as long as that is no less and at most 2^V_SLACK above what the tile wants
+// (a change rescales O), and falls by 2^V_FALL at most, which keeps O in fp32's range.  A key more than 2^V_SPREAD below
+// it has a power of its own, at most 2^V_KEY further down, and the weights of such a tile's keys are scaled the other way: a
+// token of large values takes no precision from the others, whether or not a row weighs it.
+constexpr int V_SLACK = 3, V_FALL = 64, V_SPREAD = 6, V_KEY = 16;
 
 struct PairSeg {
   int32_t b, h, rt;      // request, KV head, pair of row tiles
@@ -83,13 +89,16 @@ struct PromptSmem {
   struct Ctrl {
     uint64_t raw_full[2], raw_empty[2], scale_full[4], k_full[2], k_empty[2], v_full, v_empty;
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_free[2], drain[2];
-    int64_t sums[THREADS / 32];
+    union {
+      int64_t sums[THREADS / 32];  // until the line is scanned
+      uint8_t v_key[4][TK];        // tiles of spread values: biased exponents of what a key's weight is scaled by
+    };
     int32_t nan_from[NAN_RING][4];  // per segment: first key whose value group is NaN
     uint32_t raw_have[2];           // copies made
-    uint32_t have[4];               // blocks of 16 keys of a tile that hold keys
+    uint32_t have[4];               // blocks of 16 keys of a tile that hold keys; bit 8: its values are spread
     float k_scale[4];               // power of two taken out of the tile's keys
     int32_t v_exp[4];               // exponent taken out of the values
-    int32_t warp_exp[2][4];
+    int32_t warp_exp[3][4];
     uint32_t tmem;
     int32_t abort, bad;
   };
@@ -483,7 +492,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
                                            mbar_wait(&ct.scale_full[kt & 3], (kt >> 2) & 1, abort));
           if (!ok) break;
           const float sc = fmaxf(row_scale * ct.k_scale[kt & 3], 0x1p-126f);  // not 0: it meets -inf below
-          const uint32_t have = ct.have[kt & 3];
+          const uint32_t have = ct.have[kt & 3] & 0xffu;
+          const bool spread = ct.have[kt & 3] >> 8;
           const int v_new = ct.v_exp[kt & 3], tok = (from + j) * TK;
           tc_fence_after();
           float sv[128];
@@ -520,7 +530,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
             resc = true;
           }
           if (j > 0 && __any_sync(0xffffffffu, resc)) {  // S complete: so is the P V before it
-            // exponents are at most 2^110 and at least 2^-119 apart: two steps of a power of two
+            // exponents lie within [-119, 110], and a fall is at most V_FALL: two steps of a power of two
             const int d = v_exp - v_new;
             const float f = alpha * pow2(max(d / 2, -120)) * pow2(max(d - d / 2, -120));
 #pragma unroll 1
@@ -537,26 +547,31 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
           const float nb = m_used == NEG_INF ? 0.f : -m_used;
           const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(nb, nb);
           float2 rs2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          // ROUNDED: the fused product is exact where the maximum is rounded.  Above 2^24 the difference, half a
-          // last place of the maximum, would reach the exponent's range: scores are rounded first there.
-          const auto weights = [&](auto rounded) {
+          // CAREFUL: scores are rounded first, and a key's weight is scaled by the power of two that its values are
+          // up.  The fused product is exact where the maximum is rounded: above 2^24 the difference, half a last
+          // place of the maximum, would reach the exponent's range.
+          const auto weights = [&](auto careful) {
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
               uint32_t pk[16];
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
                 const float2 s2 = make_float2(sv[32 * h + 2 * c], sv[32 * h + 2 * c + 1]);
-                const float2 x = decltype(rounded)::value
+                const float2 x = decltype(careful)::value
                                      ? make_float2(__fmul_rn(s2.x, sc) + nb, __fmul_rn(s2.y, sc) + nb)
                                      : __ffma2_rn(s2, sc2, nb2);
-                const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                float2 e = make_float2(ex2(x.x), ex2(x.y));
                 rs2[c & 1] = __fadd2_rn(rs2[c & 1], e);
+                if (decltype(careful)::value && spread) {
+                  const uint32_t k = *reinterpret_cast<const uint16_t*>(&ct.v_key[kt & 3][32 * h + 2 * c]);
+                  e.x *= __uint_as_float((k & 255u) << 23), e.y *= __uint_as_float((k >> 8) << 23);
+                }
                 pk[c] = half2_bits(e.x, e.y);
               }
               tmem_st16(s_own + 16 * h, pk);
             }
           };
-          if (__any_sync(0xffffffffu, fabsf(nb) > 0x1p24f)) weights(std::true_type{});
+          if (spread || __any_sync(0xffffffffu, fabsf(nb) > 0x1p24f)) weights(std::true_type{});
           else weights(std::false_type{});
           l = l * alpha + ((rs2[0].x + rs2[1].x) + (rs2[0].y + rs2[1].y));
           tmem_wait_st();
@@ -575,7 +590,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
       // ---- the row, to O or to the workspace ----
       const bool whole = s.first >= t0 && s.first + s.count <= t1;
       const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-      const float f = inv * pow2(v_exp / 2) * pow2(v_exp - v_exp / 2);
+      const float f = inv * pow2(v_exp / 2), f2 = pow2(v_exp - v_exp / 2);  // of tiny values their product may underflow
       float* part = pair_part(a, blockIdx.x, s.first >= t0 ? 1 : 0) + (st * 128 + t) * PART;
       __nv_bfloat16* out = a.O + (int64_t)hd * a.o_head + (int64_t)(s.q0 + token) * a.o_row;
 #pragma unroll
@@ -599,7 +614,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
           float y[8];  // channels 8 (4 c + k) ..: columns hold them in the order 0 4 1 5 2 6 3 7
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float x = __uint_as_float(oa[8 * k + e]) * f;
+            const float x = __uint_as_float(oa[8 * k + e]) * f * f2;
             y[(e & 1) * 4 + (e >> 1)] = nan ? __int_as_float(0x7fffffff) : x;
           }
           if (live && whole)
@@ -639,7 +654,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
     };
 
     // scales of tile kt: the powers of two, and each row's (step, lo) in fp16; then its keys
-    int v_exp = -119;
+    int v_exp = -119, v_top = -119;
     const auto keys = [&](const PairSeg& s, int tile, uint32_t kt, int ring) {
       const bool there = mbar_wait(&ct.raw_full[kt & 1], (kt >> 1) & 1, abort);
       const uint8_t* raw = smem + S::RAW + (kt & 1) * S::TILE;
@@ -669,13 +684,24 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
       // powers of two to take out
       const auto exponent = [](float x, int off) { return (int)(__float_as_uint(x) >> 23) - off; };
       const int ke_own = __reduce_max_sync(0xffffffffu, max(exponent(smax, 118), exponent(lmax, 140)));
-      const int ve_own = __reduce_max_sync(0xffffffffu, exponent(vmax, 120));
-      if (lane == 0) ct.warp_exp[0][w4] = ke_own, ct.warp_exp[1][w4] = ve_own;
+      const int ve = exponent(vmax, 120);  // below -119: zeros (or nearly), which no power of two matters to
+      const int ve_own = __reduce_max_sync(0xffffffffu, ve);
+      const int ve_least = __reduce_min_sync(0xffffffffu, ve < -119 ? 1000 : ve);
+      if (lane == 0) ct.warp_exp[0][w4] = ke_own, ct.warp_exp[1][w4] = ve_own, ct.warp_exp[2][w4] = ve_least;
       sync_deq();
       const auto all4 = [](const int32_t* x) { return max(max(x[0], x[1]), max(x[2], x[3])); };
-      const int ke = min(max(all4(ct.warp_exp[0]), -119), 110);
-      v_exp = max(v_exp, min(max(all4(ct.warp_exp[1]), -119), 110));
-      const float kn = pow2(-ke), vn = pow2(-v_exp);
+      const int ke = min(max(all4(ct.warp_exp[0]), -119), 110), ve_tile = min(all4(ct.warp_exp[1]), 110);
+      v_top = max(v_top, ve_tile);
+      if (ve_tile > v_exp || (ve_tile >= -119 && ve_tile < v_exp - V_SLACK)) v_exp = max(ve_tile, v_top - V_FALL);
+      const int32_t* least = ct.warp_exp[2];
+      const bool spread = min(min(least[0], least[1]), min(least[2], least[3])) < v_exp - V_SPREAD;
+      int v_down = 0;  // of this key below v_exp
+      if (spread) {
+        if (ve >= -119) v_down = min(max(v_exp - ve, 0), V_KEY);
+        ct.v_key[kt & 3][d] = (uint8_t)(127 - v_down);
+        sync_deq();
+      }
+      const float kn = pow2(-ke), vn = pow2(v_down - v_exp);
       uint32_t* v_const = k_const + (1 + (kt & 1)) * TK * NG;
       float mid[NG];
 #pragma unroll
@@ -690,7 +716,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
         for (int b = 0; b < TK / 16; ++b)
           have |= (uint32_t)(tile * TK + 16 * b >= seen || (made >> (b >> copy16) & 1u)) << b;
         // the place of the tile before the three last: every row has handed that one's P on
-        ct.have[kt & 3] = have;
+        ct.have[kt & 3] = have | (uint32_t)spread << 8;
         ct.k_scale[kt & 3] = pow2(ke);
         ct.v_exp[kt & 3] = v_exp;
         mbar_arrive(&ct.scale_full[kt & 3]);
@@ -775,7 +801,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
       // values of the pair after the next one are
       if (d < 4) ct.nan_from[ring][d] = 0x7fffffff;
       sync_deq();
-      v_exp = -119;
+      v_exp = v_top = -119;
       // K(0), then K(j + 1), V(j): values have one buffer, free once both streams' P V before are done
       ok = all_deq(keys(s, from, kt, ring));
       if (ok) take_values(kt);

@@ -101,3 +101,26 @@ def test_keys_far_below_a_sink_still_weigh(kv, gap, at, max_q):
     o, O = _compare(cache, table, K, V, Q, scale, max_q, lost, 2.0 ** -32 if max_q == MANY else 2.0 ** -31)
     # the roundings of 32768 weights and more average out: of the norm, O's own is left
     assert float((o.double() - O).norm() / O.norm()) < 2.0 ** -8 + 2.0 ** -10
+
+
+@pytest.mark.parametrize("max_q", [1, MANY])
+@pytest.mark.parametrize("far", [2.0 ** 12, 2.0 ** 20, 2.0 ** -20])
+@pytest.mark.parametrize("at,group", [(0, 64), (777, 128), (1000, 32), (2999, 64)])
+def test_a_value_of_another_size_leaves_the_others_as_they_are(at, group, far, max_q):
+    """One token's values are `far` times the others'; no row weighs it (its score is 28 nats below zero, or it is the
+    last key, which only the last row sees), or nearly.  Values keep their own precision: fp16's 11 bits of each, or half
+    a subnormal step, 2^-25; a key's largest value is scaled to 2^-13 at least, so 2^-12 of that (few rows: fp32).  The
+    weights of the keys in the outlier's own tile are scaled down with it: 2^-32 of the outlier (few rows: 2^-31, of all
+    keys; `kv` of them bound both)."""
+    kv = 3000
+    g = torch.Generator(device="cuda").manual_seed(at)
+    Q = torch.randn(2, 5, 128, generator=g, device="cuda")
+    K = torch.randn(1, kv, 128, generator=g, device="cuda")
+    V = torch.randn(1, kv, 128, generator=g, device="cuda")
+    Q[..., 0], K[..., 0] = 4.0, 0.0
+    K[0, at], V[0, at] = 0.0, far * (1 + torch.rand(128, generator=g, device="cuda"))
+    K[0, at, 0] = -20.0
+    Q, K, V = (x.to(torch.bfloat16) for x in (Q, K, V))
+    cache, table = _filled(K, V, 64, group)
+    own = V.double().abs()[0].amax(-1) * 2.0 ** -12
+    _compare(cache, table, K, V, Q, 0.35, max_q, own, 2.0 ** -32 if max_q == MANY else 2.0 ** -31)
