@@ -8,12 +8,13 @@
 // warpgroups hold a query row per thread: maximum, exponentials and sums in fp32, O rescaled only
 // when the maximum grows by 2^8 or the values' power of two changes.
 //
-// Scores keep fp32's precision: the operands are exact.  A code less 8 has 3 bits (or is 8, a power of
+// Scores keep fp32's precision: the operands are exact, as long as the steps of a key's groups lie within 2^4 of
+// one another (below, they lose what is under 2^-12 of the largest).  A code less 8 has 3 bits (or is 8, a power of
 // two) and a step has 8, so (code - 8) * step fits fp16's 11 bits; what is left, lo + 8 step per group,
 // meets the group's sum of the query in 16 more columns, each of the two as a sum of two fp16 parts
 // (three of their four products).  A power of two is taken out of each tile's keys and each query row,
-// so that fp16's range holds them.  (Keys rounded to fp16 put a score off by 3e-4, 30 times what lse
-// may lose.)  Values are lo + code * step rounded to fp16's 11 bits: O is rounded to 8.
+// so that fp16's range holds them, and out of single keys where they differ much.  (Keys rounded to fp16 put a
+// score off by 3e-4, 30 times what lse may lose.)  Values are lo + code * step rounded to fp16's 11 bits: O is rounded to 8.
 //
 // Work: the 256-row pairs of a request see more and more keys; pair f and pair (last - f) together see
 // nearly the same number, so a request's units (tiles, and one more per pair for its start and end)
@@ -68,7 +69,11 @@ constexpr int DEQ_UNROLL = 2;
 // (a change rescales O), and falls by 2^V_FALL at most, which keeps O in fp32's range.  A key more than 2^V_SPREAD below
 // it has a power of its own, at most 2^V_KEY further down, and the weights of such a tile's keys are scaled the other way: a
 // token of large values takes no precision from the others, whether or not a row weighs it.
-constexpr int V_SLACK = 3, V_FALL = 64, V_SPREAD = 6, V_KEY = 16;
+constexpr int V_SLACK = 3, V_FALL = 64, V_SPREAD = 6;
+// Keys likewise: steps of a tile's largest key lie in [2^-9, 2^-8), and (code - 8) * step is exact down to steps of
+// 2^-17.  A key more than 2^K_SPREAD below the largest has a power of its own, which its scores take back.
+constexpr int K_SPREAD = 4;
+constexpr int KEY_DOWN = 15;  // the most that a key's own power is below its tile's: half a byte each for K and V
 
 struct PairSeg {
   int32_t b, h, rt;      // request, KV head, pair of row tiles
@@ -91,14 +96,14 @@ struct PromptSmem {
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_free[2], drain[2];
     union {
       int64_t sums[THREADS / 32];  // until the line is scanned
-      uint8_t v_key[4][TK];        // tiles of spread values: biased exponents of what a key's weight is scaled by
+      uint8_t key_down[4][TK];     // spread tiles: how far a key's own powers of two are down (K low, V high half)
     };
     int32_t nan_from[NAN_RING][4];  // per segment: first key whose value group is NaN
     uint32_t raw_have[2];           // copies made
-    uint32_t have[4];               // blocks of 16 keys of a tile that hold keys; bit 8: its values are spread
+    uint32_t have[4];               // blocks of 16 keys of a tile that hold keys; bit 8: it is spread
     float k_scale[4];               // power of two taken out of the tile's keys
     int32_t v_exp[4];               // exponent taken out of the values
-    int32_t warp_exp[3][4];
+    int32_t warp_exp[2][4];
     uint32_t tmem;
     int32_t abort, bad;
   };
@@ -492,8 +497,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
                                            mbar_wait(&ct.scale_full[kt & 3], (kt >> 2) & 1, abort));
           if (!ok) break;
           const float sc = fmaxf(row_scale * ct.k_scale[kt & 3], 0x1p-126f);  // not 0: it meets -inf below
-          const uint32_t have = ct.have[kt & 3] & 0xffu;
-          const bool spread = ct.have[kt & 3] >> 8;
+          const uint32_t have = ct.have[kt & 3];
           const int v_new = ct.v_exp[kt & 3], tok = (from + j) * TK;
           tc_fence_after();
           float sv[128];
@@ -505,14 +509,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
 #pragma unroll
             for (int c = 0; c < 128; ++c) sv[c] = __uint_as_float(rr[c >> 5][c & 31]);
           }
-          if (__any_sync(0xffffffffu, tok + TK > lim)) {
+          if (__any_sync(0xffffffffu, tok + TK > lim) || have != 0xffu) {
             const int open = lim - tok;  // columns this row sees
+            if (have >> 8)
 #pragma unroll
-            for (int c = 0; c < 128; ++c) sv[c] = c < open ? sv[c] : NEG_INF;
-          }
-          if (have != 0xffu) {  // keys on no page
+              for (int c = 0; c < 128; ++c) sv[c] *= pow2(-(int)(ct.key_down[kt & 3][c] & 15u));
 #pragma unroll
-            for (int c = 0; c < 128; ++c) sv[c] = (have >> (c >> 4)) & 1u ? sv[c] : NEG_INF;
+            for (int c = 0; c < 128; ++c)  // and is on a page
+              sv[c] = c < open && ((have >> (c >> 4)) & 1u) ? sv[c] : NEG_INF;
           }
           float m4[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
@@ -562,16 +566,16 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
                                      : __ffma2_rn(s2, sc2, nb2);
                 float2 e = make_float2(ex2(x.x), ex2(x.y));
                 rs2[c & 1] = __fadd2_rn(rs2[c & 1], e);
-                if (decltype(careful)::value && spread) {
-                  const uint32_t k = *reinterpret_cast<const uint16_t*>(&ct.v_key[kt & 3][32 * h + 2 * c]);
-                  e.x *= __uint_as_float((k & 255u) << 23), e.y *= __uint_as_float((k >> 8) << 23);
+                if (decltype(careful)::value && (have >> 8)) {
+                  e.x *= pow2(-(int)(ct.key_down[kt & 3][32 * h + 2 * c] >> 4));
+                  e.y *= pow2(-(int)(ct.key_down[kt & 3][32 * h + 2 * c + 1] >> 4));
                 }
                 pk[c] = half2_bits(e.x, e.y);
               }
               tmem_st16(s_own + 16 * h, pk);
             }
           };
-          if (spread || __any_sync(0xffffffffu, fabsf(nb) > 0x1p24f)) weights(std::true_type{});
+          if (__any_sync(0xffffffffu, (have >> 8) || fabsf(nb) > 0x1p24f)) weights(std::true_type{});
           else weights(std::false_type{});
           l = l * alpha + ((rs2[0].x + rs2[1].x) + (rs2[0].y + rs2[1].y));
           tmem_wait_st();
@@ -653,6 +657,16 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
       return r != 0;
     };
 
+    const auto any_deq = [](uint32_t x) {
+      uint32_t r;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+          : "=r"(r)
+          : "r"(x)
+          : "memory");
+      return r != 0;
+    };
+
     // scales of tile kt: the powers of two, and each row's (step, lo) in fp16; then its keys
     int v_exp = -119, v_top = -119;
     const auto keys = [&](const PairSeg& s, int tile, uint32_t kt, int ring) {
@@ -683,25 +697,19 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
       // steps come below 2^-8 (2^24 steps fit fp16), lo below 2^14, values below 2^-6: exponents of the
       // powers of two to take out
       const auto exponent = [](float x, int off) { return (int)(__float_as_uint(x) >> 23) - off; };
-      const int ke_own = __reduce_max_sync(0xffffffffu, max(exponent(smax, 118), exponent(lmax, 140)));
-      const int ve = exponent(vmax, 120);  // below -119: zeros (or nearly), which no power of two matters to
-      const int ve_own = __reduce_max_sync(0xffffffffu, ve);
-      const int ve_least = __reduce_min_sync(0xffffffffu, ve < -119 ? 1000 : ve);
-      if (lane == 0) ct.warp_exp[0][w4] = ke_own, ct.warp_exp[1][w4] = ve_own, ct.warp_exp[2][w4] = ve_least;
+      const int ko = max(exponent(smax, 118), exponent(lmax, 140)), vo = exponent(vmax, 120);  // of this key
+      const int k_top = __reduce_max_sync(0xffffffffu, ko), v_high = __reduce_max_sync(0xffffffffu, vo);
+      if (lane == 0) ct.warp_exp[0][w4] = k_top, ct.warp_exp[1][w4] = v_high;
       sync_deq();
       const auto all4 = [](const int32_t* x) { return max(max(x[0], x[1]), max(x[2], x[3])); };
-      const int ke = min(max(all4(ct.warp_exp[0]), -119), 110), ve_tile = min(all4(ct.warp_exp[1]), 110);
-      v_top = max(v_top, ve_tile);
-      if (ve_tile > v_exp || (ve_tile >= -119 && ve_tile < v_exp - V_SLACK)) v_exp = max(ve_tile, v_top - V_FALL);
-      const int32_t* least = ct.warp_exp[2];
-      const bool spread = min(min(least[0], least[1]), min(least[2], least[3])) < v_exp - V_SPREAD;
-      int v_down = 0;  // of this key below v_exp
-      if (spread) {
-        if (ve >= -119) v_down = min(max(v_exp - ve, 0), V_KEY);
-        ct.v_key[kt & 3][d] = (uint8_t)(127 - v_down);
-        sync_deq();
-      }
-      const float kn = pow2(-ke), vn = pow2(v_down - v_exp);
+      const int ke = min(max(all4(ct.warp_exp[0]), -119), 110), ve = min(all4(ct.warp_exp[1]), 110);  // of the tile
+      v_top = max(v_top, ve);
+      if (ve > v_exp || (ve >= -119 && ve < v_exp - V_SLACK)) v_exp = max(ve, v_top - V_FALL);
+      // how far this key's own powers are down; zeros (or nearly: -118, -120) have none
+      const int k_down = ko >= -117 && ko < ke - K_SPREAD ? min(ke - ko, KEY_DOWN) : 0;
+      const int v_down = vo >= -119 && vo < v_exp - V_SPREAD ? min(v_exp - vo, KEY_DOWN) : 0;
+      ct.key_down[kt & 3][d] = (uint8_t)(k_down | v_down << 4);
+      const float kn = pow2(k_down - ke), vn = pow2(v_down - v_exp);
       uint32_t* v_const = k_const + (1 + (kt & 1)) * TK * NG;
       float mid[NG];
 #pragma unroll
@@ -711,17 +719,17 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
         v_const[d * NG + gr] = half2_bits(bf_lo(vw[gr]) * vn * 16777216.f, bf_hi(vw[gr]) * vn);
         mid[gr] = fmaf(8.f, step, bf_hi(kw[gr]) * kn);
       }
+      const bool spread = any_deq(k_down | v_down);  // the scales are written
       if (d == 0) {
-        uint32_t have = 0;
+        uint32_t have = (uint32_t)spread << 8;
         for (int b = 0; b < TK / 16; ++b)
           have |= (uint32_t)(tile * TK + 16 * b >= seen || (made >> (b >> copy16) & 1u)) << b;
         // the place of the tile before the three last: every row has handed that one's P on
-        ct.have[kt & 3] = have | (uint32_t)spread << 8;
+        ct.have[kt & 3] = have;
         ct.k_scale[kt & 3] = pow2(ke);
         ct.v_exp[kt & 3] = v_exp;
         mbar_arrive(&ct.scale_full[kt & 3]);
       }
-      sync_deq();
       if (!there || (kt >= 2 && !mbar_wait(&ct.k_empty[kt & 1], ((kt >> 1) - 1) & 1, abort))) return false;
       uint8_t* dst = smem + S::K + (kt & 1) * Q_BYTES;
       {

@@ -44,9 +44,10 @@ def _compare(cache, table, K, V, Q, scale, max_q, v_error, weight_error, B=200):
     """K, V [1, kv, 128], Q [H, n, 128]; the last n keys are the queries' own.  B requests hold the same keys and ask the
     same: with more of them than SMs a CTA walks over whole contexts, and what it sums up is not cut into short pieces.  What a kernel may be off by, with p the
     weights and m the largest of them (the sums are over a row's keys):
-      scores: ko.tolerance's bound of fp32 sums (136 of them, 2^-24 each), times the largest sum of magnitudes, and for
-        the many-row kernel 2^-16 of the largest step per channel (fp16's subnormals): a relative error of every weight,
-        twice (numerator and denominator), with the exponential's 2^-21 and the sums' n / 2 * 2^-24;
+      scores: ko.tolerance's bound of fp32 sums (136 of them, 2^-24 each) times the largest sum of magnitudes behind a key
+        that weighs anything: a relative error of every weight, twice (numerator and denominator), with the exponential's
+        2^-21 and the sums' n / 2 * 2^-24.  The many-row kernel's key operands are exact: a key's steps are within 2^4 of
+        one another here;
       weights: in fp16, 2^-11 relative and at least weight_error of m, times the largest magnitude of a value;
       values: v_error[j], of every value of key j, and 2^-11 relative;
       O: rounded to bf16, 2^-8."""
@@ -57,9 +58,8 @@ def _compare(cache, table, K, V, Q, scale, max_q, v_error, weight_error, B=200):
     see = torch.arange(kv, device="cuda")[None] <= kv - n + torch.arange(n, device="cuda")[:, None]
     s = s.masked_fill(~see, float("-inf"))
     p = torch.softmax(s, -1)
-    reach = (q.abs() @ (kl.abs() + 15 * ks)[0].T).amax(-1, keepdim=True) * scale
-    if max_q == MANY:
-        reach = reach + ks.max() * q.abs().sum(-1, keepdim=True) * scale
+    assert ((ks == 0) | (ks * 16 >= ks.amax(-1, keepdim=True))).all()
+    reach = (q.abs() @ (kl.abs() + 15 * ks)[0].T).masked_fill(p == 0, 0).amax(-1, keepdim=True) * scale
     ds = reach * 2.0 ** -16 + 2.0 ** -21 + (kv / 2 + 32) * 2.0 ** -24
     mag = v.abs()[0] if max_q == MANY else ((vl + 8 * vs).abs() + 8 * vs)[0]  # few rows: codes less 8 beside lo + 8 step
     O = p @ v[0]
@@ -120,6 +120,25 @@ def test_a_value_of_another_size_leaves_the_others_as_they_are(at, group, far, m
     Q[..., 0], K[..., 0] = 4.0, 0.0
     K[0, at], V[0, at] = 0.0, far * (1 + torch.rand(128, generator=g, device="cuda"))
     K[0, at, 0] = -20.0
+    Q, K, V = (x.to(torch.bfloat16) for x in (Q, K, V))
+    cache, table = _filled(K, V, 64, group)
+    own = V.double().abs()[0].amax(-1) * 2.0 ** -12
+    _compare(cache, table, K, V, Q, 0.35, max_q, own, 2.0 ** -32 if max_q == MANY else 2.0 ** -31)
+
+
+@pytest.mark.parametrize("max_q", [1, MANY])
+@pytest.mark.parametrize("far", [2.0 ** 12, 2.0 ** 20, 2.0 ** -20])
+@pytest.mark.parametrize("at,group", [(0, 64), (777, 128), (1000, 32), (2999, 64)])
+def test_a_key_of_another_size_leaves_the_others_as_they_are(at, group, far, max_q):
+    """One key is `far` times the others and weighs nothing (its score is below -28 far; the last key is seen by the last
+    row alone), or it is as small and weighs as much as a key of zeros.  The others' scores keep fp32's precision."""
+    kv = 3000
+    g = torch.Generator(device="cuda").manual_seed(at + 1)
+    Q = torch.randn(2, 5, 128, generator=g, device="cuda")
+    K = torch.randn(1, kv, 128, generator=g, device="cuda")
+    V = torch.randn(1, kv, 128, generator=g, device="cuda")
+    Q[..., 0], K[0, at, 0] = 4.0, -40.0
+    K[0, at] *= far
     Q, K, V = (x.to(torch.bfloat16) for x in (Q, K, V))
     cache, table = _filled(K, V, 64, group)
     own = V.double().abs()[0].amax(-1) * 2.0 ** -12
