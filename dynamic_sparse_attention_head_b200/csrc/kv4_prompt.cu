@@ -388,6 +388,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
         const int n = tiles_to(s) - tiles_from(s);
         if (n <= 0) continue;
         if (rows_of(s, st) <= 0) {  // the pair has no rows for this stream: only hand the tiles on
+          // (not before the rows of the stream's last pair have left: the widening warps, which what is handed on here
+          // lets run ahead, reuse what those rows still read)
+          ok = done == 0 || mbar_wait(&ct.o_free[st], (done - 1) & 1, abort);
           for (int j = 0; j < n && ok; ++j, ++kt) {
             ok = mbar_wait(&ct.k_full[kt & 1], (kt >> 1) & 1, abort);
             if (ok) mbar_arrive(&ct.k_empty[kt & 1]);
@@ -597,6 +600,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
       const float f = inv * pow2(v_exp / 2), f2 = pow2(v_exp - v_exp / 2);  // of tiny values their product may underflow
       float* part = pair_part(a, blockIdx.x, s.first >= t0 ? 1 : 0) + (st * 128 + t) * PART;
       __nv_bfloat16* out = a.O + (int64_t)hd * a.o_head + (int64_t)(s.q0 + token) * a.o_row;
+      uint32_t nans = 0;  // value groups that are NaN from some key on that this row sees; read before O is given back
+      if (n > 0)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) nans |= (uint32_t)(ct.nan_from[ring][c] < lim) << c;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t oa[32];
@@ -611,8 +618,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
 #pragma unroll
           for (int e = 0; e < 32; ++e) oa[e] = 0u;
         }
-        // a value group that is NaN from some key on that this row sees
-        const bool nan = n > 0 && ct.nan_from[ring][c] < lim;
+        const bool nan = (nans >> c) & 1u;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           float y[8];  // channels 8 (4 c + k) ..: columns hold them in the order 0 4 1 5 2 6 3 7
@@ -805,8 +811,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
       const int from = tiles_from(s), n = tiles_to(s) - from;
       if (n <= 0) continue;
       const int ring = segs++ & (NAN_RING - 1);
-      // the ring's place was last read four segments ago: a row pair's output is done before the
-      // values of the pair after the next one are
+      // The ring's place was last used four segments ago.  Before they came here these warps waited until both streams
+      // had handed on a tile of one of the two segments before this one, and a stream does that, with rows or without,
+      // only once the rows of its last pair have read their place and given O back.
       if (d < 4) ct.nan_from[ring][d] = 0x7fffffff;
       sync_deq();
       v_exp = v_top = -119;

@@ -150,3 +150,24 @@ def test_a_key_of_another_size_leaves_the_others_as_they_are(at, group, far, max
     Q, K, V = (x.to(torch.bfloat16) for x in (Q, K, V))
     cache, table = _filled(K, V, 64, group)
     _compare(cache, table, K, V, Q, 0.35, max_q, *_losses(V, max_q))
+
+
+def test_nan_values_reach_the_second_stream_before_pairs_without_one():
+    """Pairs of more than 128 rows, whose last keys hold a NaN value group, followed by many of at most 128 rows, which
+    leave the second stream of rows without work: what the first pair's rows still read is not reused."""
+    kv, group, page, B = 300, 64, 64, 1000
+    K, V = (torch.randn(1, kv, 128, generator=torch.Generator().manual_seed(i)).to(torch.bfloat16).cuda() for i in (1, 2))
+    V[0, kv - 60, 70] = float("nan")
+    cache, table = _filled(K, V, page, group)
+    new = torch.tensor(([200] + [100] * 5 + [129] + [1] * 4) * 100, dtype=I32)[:B]
+    cu = torch.cat((torch.zeros(1, dtype=I32), new.cumsum(0).int())).cuda()
+    T = int(cu[-1])
+    Q = torch.randn(1, T, 128, device="cuda").to(torch.bfloat16)
+    O, lse = torch.zeros_like(Q), torch.zeros(1, T, device="cuda")
+    cache.attend(Q, O, table.repeat(B, 1), torch.full((B,), kv, dtype=I32, device="cuda"), cu, MANY, 0.1, cache.alloc_workspace(), lse=lse)
+    assert cache.device_status() == 0
+    b = torch.repeat_interleave(torch.arange(B), new.long()).cuda()
+    pos = kv - new.cuda()[b] + torch.arange(T, device="cuda") - cu[b]  # a row's own key
+    sees = pos >= kv - 60
+    assert torch.equal(torch.isnan(O[0, :, 64:]), sees[:, None].expand(T, 64))
+    assert torch.isfinite(O[0, :, :64]).all() and torch.isfinite(lse).all()
