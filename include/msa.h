@@ -418,7 +418,9 @@ msa_status msa_kv4_slots(const msa_kv4_cache* cache, const int32_t* kv_lens, con
 
 /* Gives back the pages of the requests ids[0 .. n): pushed on the free stack in the order of the
  * list, their kv_lens set to 0 and their table entries to -1.  An id named twice counts once; an id
- * outside [0, B) is recorded as an error.  n <= 2048. */
+ * outside [0, B) is recorded as an error.  A table entry outside the cache is recorded and dropped: it is not
+ * pushed.  From the first request on whose pages the stack has no room for (some were given back before), none is
+ * released: lengths, table and stack stay as they were, recorded.  n <= 2048. */
 msa_status msa_kv4_release(const msa_kv4_cache* cache, const int32_t* ids, int32_t n, int32_t* kv_lens, int32_t B,
                            int32_t* block_table, int64_t table_stride, int32_t max_blocks, int32_t* free_pages,
                            int32_t* n_free, void* stream);
