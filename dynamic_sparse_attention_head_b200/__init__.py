@@ -58,8 +58,11 @@ class RopeC(ctypes.Structure):
 
 
 class KV4CacheC(ctypes.Structure):
-    _fields_ = [("pages", _P), ("n_pages", _I64), ("page_tokens", _I32), ("Hkv", _I32), ("group", _I32), ("_pad", _I32),
+    _fields_ = [("pages", _P), ("n_pages", _I64), ("page_tokens", _I32), ("Hkv", _I32), ("group", _I32), ("flags", _I32),
                 ("state", _P)]
+
+
+KV4_WHOLE_REQUESTS = 1  # msa_kv4_cache.flags
 
 
 class MsaError(RuntimeError):

@@ -82,7 +82,7 @@ struct SlotArgs {
   int32_t *block_table, *kv_out, *n_free_out, *cu_new, *positions;
   int64_t* slots;
   int64_t table_stride, capacity;
-  int32_t B, max_blocks;
+  int32_t B, max_blocks, whole;
 };
 
 // Every block scans the lengths for itself (B ints, one or a few per thread) and then takes its
@@ -137,7 +137,8 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv4_slots_kernel(const SlotArgs 
     if (b < a.B) {
       if (cn > 0x7fffffff || cp > 0x7fffffff) bad = 1;
       cum_new[b + 1] = (int32_t)min(cn, (int64_t)0x7fffffff);
-      cum_page[b + 1] = (int32_t)min(cp, (int64_t)0x7fffffff);
+      // a request that passes the map's end wants more pages than there are, and so do all after it
+      cum_page[b + 1] = a.whole && cn > a.capacity ? 0x7fffffff : (int32_t)min(cp, (int64_t)0x7fffffff);
       if (refused) kv[b] = kv[b] | (int32_t)0x80000000;
     }
     run_new += all[0];
@@ -563,6 +564,7 @@ msa_status msa_kv4_slots(const msa_kv4_cache* cache, const int32_t* kv_lens, con
   a.block_table = block_table, a.kv_out = kv_lens_out, a.n_free_out = n_free_out, a.cu_new = cu_new;
   a.positions = positions, a.slots = slots, a.table_stride = table_stride, a.capacity = capacity;
   a.B = B, a.max_blocks = max_blocks;
+  a.whole = cache->flags & MSA_KV4_WHOLE_REQUESTS;
   // one block for a decode batch; more only where there are tokens for them
   const int64_t want = (capacity + 4 * SLOT_THREADS - 1) / (4 * SLOT_THREADS);
   const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(want, 2 * sm_count()));

@@ -10,7 +10,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import KV4CacheC, RopeC, _check, _lib
+from . import KV4_WHOLE_REQUESTS, KV4CacheC, RopeC, _check, _lib
 
 try:
     from . import _binding as _native  # checks the tensors and calls the library (csrc/binding.cpp)
@@ -72,9 +72,11 @@ class KV4Cache:
     """One layer's paged 4-bit K/V cache (msa_kv4_cache): `pages` uint8 [n_pages, Hkv, kv4_page_bytes(page,
     group)] on the GPU, `page` tokens a page, `group` channels a scale.  `KV4Cache.alloc` makes the
     pages too.  Calls on one cache run in stream order (`read` and `attend` may overlap); a CUDA graph
-    may hold any of them."""
+    may hold any of them.  `whole_requests`: `slots` refuses a request whose new tokens do not all have an entry in its map,
+    and all after it, as it does where the pages run out (otherwise the map alone is cut, and the lengths go on over
+    tokens that cannot be written)."""
 
-    def __init__(self, pages, page: int = 64, group: int = 64):
+    def __init__(self, pages, page: int = 64, group: int = 64, whole_requests: bool = False):
         want = kv4_page_bytes(page, group)
         if not isinstance(pages, torch.Tensor) or pages.dtype is not torch.uint8 or pages.dim() != 3 or \
                 pages.shape[2] != want or not pages.is_contiguous() or not pages.is_cuda:
@@ -85,12 +87,14 @@ class KV4Cache:
         self.device, self._dev = pages.device, pages.get_device()
         self.state = torch.zeros(64, dtype=torch.uint8, device=pages.device)
         self._c = KV4CacheC(pages=pages.data_ptr(), n_pages=self.n_pages, page_tokens=self.page, Hkv=self.Hkv,
-                            group=self.group, state=self.state.data_ptr())
+                            group=self.group, flags=KV4_WHOLE_REQUESTS if whole_requests else 0, state=self.state.data_ptr())
         self._addr = ctypes.addressof(self._c)
 
     @classmethod
-    def alloc(cls, n_pages: int, Hkv: int, page: int = 64, group: int = 64, device="cuda") -> "KV4Cache":
-        return cls(torch.zeros(n_pages, Hkv, kv4_page_bytes(page, group), dtype=torch.uint8, device=device), page, group)
+    def alloc(cls, n_pages: int, Hkv: int, page: int = 64, group: int = 64, device="cuda",
+              whole_requests: bool = False) -> "KV4Cache":
+        return cls(torch.zeros(n_pages, Hkv, kv4_page_bytes(page, group), dtype=torch.uint8, device=device), page, group,
+                   whole_requests)
 
     def alloc_workspace(self, Hq: int = 0):
         """Zero-filled workspace of `attend` (its size does not depend on the shapes)."""
@@ -101,7 +105,8 @@ class KV4Cache:
         """msa_kv4_slots: pages for new_lens[b] more tokens per request, from the top of the free stack
         free_pages[: n_free]; fills block_table's new entries, cu_new [B + 1], slots (int64) and
         positions (int32) of the new tokens (entries behind the last are left), and kv_lens / n_free
-        (in place, or in the *_out tensors)."""
+        (in place, or in the *_out tensors).  More new tokens than `slots` holds are an error of device_status(); see
+        `whole_requests`."""
         code = _native.slots(self._addr, self._dev, kv_lens, new_lens, block_table, free_pages, n_free, slots, positions,
                              cu_new, kv_lens_out, n_free_out, None if stream is None else stream.cuda_stream)
         if code:

@@ -391,9 +391,16 @@ typedef struct {
   int32_t page_tokens;  /* 16, 32, 64, 128 or 256 */
   int32_t Hkv;          /* 1 .. 1024 */
   int32_t group;        /* 32, 64 or 128 */
-  int32_t _pad;
+  int32_t flags;        /* 0, or MSA_KV4_WHOLE_REQUESTS */
   void* state;          /* device, 64 bytes, 16-byte aligned */
 } msa_kv4_cache;
+
+/* msa_kv4_slots: a request whose new tokens do not all lie below `capacity` is refused, like one that the free pages
+ * do not suffice for, and so are all after it.  Without the flag the map alone is cut: the request is given its
+ * pages and its length advances over tokens that have no slot.  Those cannot be written, and attention over that
+ * length reads what the pages held before, another request's rows, say: a caller that lets tokens pass the
+ * capacity reads msa_kv4_status before it uses the lengths. */
+#define MSA_KV4_WHOLE_REQUESTS 1
 
 /* Bytes of one page of one KV head: page_tokens * (128 + 8 * 128 / group); 0 for sizes the cache
  * does not have. */
@@ -405,8 +412,8 @@ size_t msa_kv4_page_bytes(int32_t page_tokens, int32_t group);
  * top of the stack free_pages[0 .. *n_free) (int32, room for n_pages entries), in the order of the requests,
  * and written to its row.  Outputs: kv_lens_out[b] = kv_lens[b] + new_lens[b], *n_free_out (each may
  * be its input), cu_new[B + 1] (running sum of new_lens), and for token t of cu_new[b] + i: slots[t]
- * (int64) and positions[t] = kv_lens[b] + i, for t below `capacity`; entries behind the last token
- * are left as they were.
+ * (int64) and positions[t] = kv_lens[b] + i, for t below `capacity` (a token at or behind it is recorded as an error, see
+ * MSA_KV4_WHOLE_REQUESTS); entries behind the last token are left as they were.
  * A request that does not fit its row (or has a negative length; negative new tokens count as
  * none) gets no pages; from the first request on that the free pages do not suffice for, none
  * does: their slots are -1, kv_lens_out = kv_lens, and the error is recorded (msa_kv4_status).

@@ -76,3 +76,65 @@ def test_release_of_many_pages_with_and_without_broken_entries():
         for b in named:
             left[b, :-(-lens[b] // page)] = -1
         assert t.tolist() == left.tolist()
+
+
+@pytest.mark.parametrize("alias", [False, True])
+@pytest.mark.parametrize("kv,new,cap,kept", [
+    ([0, 4, 5], [20, 30, 2], 25, 1),          # the second passes the map's end
+    ([0, 4, 5], [20, 30, 2], 50, 2),          # the third is behind it
+    ([0, 4, 5], [20, 30, 2], 52, 3),          # all just fit
+    ([7, 0], [3, 1], 0, 0),
+    ([7, 0, 9], [0, 0, 4], 0, 2),             # requests without tokens need no entry
+    ([15] * 300, [3] * 300, 620, 206),
+    ([0, 17, 0, 400], [30000, 1, 0, 20011], 30001, 3),  # over several blocks
+])
+def test_whole_requests_are_refused_where_the_map_ends(kv, new, cap, kept, alias):
+    page, B = 16, len(kv)
+    blocks = max(-(-(k + n) // page) for k, n in zip(kv, new))
+    held = [-(-k // page) for k in kv]
+    n_pages = sum(held) + sum(-(-n // page) + 1 for n in new)
+    cache = msa.KV4Cache.alloc(n_pages, 1, page, 128, whole_requests=True)
+    table, at = np.full((B, blocks), -1), 0
+    for b, h in enumerate(held):
+        table[b, :h] = np.arange(at, at + h)
+        at += h
+    t, free, nf = _ints(table), _ints(list(range(at, n_pages)) + [0] * at), _ints([n_pages - at])
+    k, n = _ints(kv), _ints(new)
+    ko, nfo = (k, nf) if alias else (torch.zeros_like(k), torch.zeros_like(nf))
+    sl, pos, cu = _ints([-77] * cap, torch.int64), _ints([-77] * cap), _ints([0] * (B + 1))
+    cache.slots(k, n, t, free, nf, sl, pos, cu, kv_lens_out=None if alias else ko, n_free_out=None if alias else nfo)
+    assert cache.device_status() == (BOUNDS if kept < B else 0)
+    assert ko.tolist() == [a + m if b < kept else a for b, (a, m) in enumerate(zip(kv, new))]
+    assert cu.tolist() == np.concatenate(([0], np.cumsum(new))).tolist()
+    taken = sum(-(-(a + m) // page) - -(-a // page) for a, m in list(zip(kv, new))[:kept])
+    assert nfo.tolist() == [n_pages - at - taken]
+    t = t.cpu().numpy()
+    assert (t[kept:] == table[kept:]).all()
+    want = [int(t[b, p // page]) * page + p % page if b < kept else -1 for b in range(B) for p in range(kv[b], kv[b] + new[b])]
+    assert sl.tolist() == (want + [-77] * cap)[:cap]
+    assert pos.tolist() == ([p for b in range(B) for p in range(kv[b], kv[b] + new[b])] + [-77] * cap)[:cap]
+    assert len(set(want[:int(cu[kept])])) == int(cu[kept])
+
+
+def test_a_captured_step_reads_no_other_requests_rows_where_the_map_is_too_short():
+    """Slot map, write and attention of a step in one graph, two new tokens where the map has room for one: the pages of the
+    second request, released by one whose values were 100, are not read."""
+    page, group = 16, 64
+    cache = msa.KV4Cache.alloc(4, 1, page, group, whole_requests=True)
+    x = torch.full((1, 32, 128), 100.0, dtype=torch.bfloat16, device="cuda")
+    table, kv = _ints([[0], [1]]), _ints([16, 16])
+    cache.append(x, x, torch.arange(32, device="cuda"))
+    free, nf = _ints([2, 3, -1, -1]), _ints([0])
+    cache.release(_ints([0, 1]), kv, table, free, nf)
+    x = torch.ones(1, 1, 128, dtype=torch.bfloat16, device="cuda")
+    sl, pos, cu, one = _ints([0], torch.int64), _ints([0]), _ints([0, 0, 0]), _ints([1, 1])
+    q, ws = torch.ones(1, 2, 128, dtype=torch.bfloat16, device="cuda"), cache.alloc_workspace()
+    o = torch.full_like(q, 7.0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.slots(kv, one, table, free, nf, sl, pos, cu)
+        cache.append(x, x, sl)
+        cache.attend(q, o, table, kv, cu, 1, 0.1, ws)
+    graph.replay()
+    assert kv.tolist() == [1, 0] and nf.tolist() == [1] and cache.device_status() == BOUNDS
+    assert (o[0, 0] == 1).all() and (o[0, 1] == 0).all()
