@@ -134,6 +134,13 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
   return nullptr;
 }
 
+// Python's other threads run while the library is in the call: a status call waits for the stream, and a launch for room
+// in the queue.  The arguments live on in the caller's frame; every one is taken apart before.
+struct Unlocked {
+  PyThreadState* const state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // Q, K, Qo, Ko, positions, rope (address), axes, wq, wk, eps, stream
 PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 11, [&] {
@@ -154,10 +161,13 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     in.q_head = Q.stride(0), in.q_row = Q.stride(1), in.k_head = K.stride(0), in.k_row = K.stride(1);
     out.q_head = Qo.stride(0), out.q_row = Qo.stride(1), out.k_head = Ko.stride(0), out.k_row = Ko.stride(1);
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    const float eps = (float)number(a[9], "eps");
+    const msa_rope rope = *static_cast<const msa_rope*>(address(a[5]));
+    void* const st = stream_of(a[10], dev);
+    const Unlocked u;
     return msa_qk_norm_rope(Q.data_ptr(), K.data_ptr(), &in, Qo.data_ptr(), Ko.data_ptr(), &out, T, (int32_t)Q.size(0),
-                            (int32_t)K.size(0), wq, wk, (float)number(a[9], "eps"),
-                            static_cast<const msa_rope*>(address(a[5])), ptr<const int32_t>(pos),
-                            pos.dim() == 2 ? pos.stride(0) : T, stream_of(a[10], dev));
+                            (int32_t)K.size(0), wq, wk, eps, &rope, ptr<const int32_t>(pos),
+                            pos.dim() == 2 ? pos.stride(0) : T, st);
   });
 }
 
@@ -176,9 +186,11 @@ PyObject* slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& kv_out = a[10] == Py_None ? kv : vec(a[10], "kv_lens_out", at::kInt, k.dev, B);
     const at::Tensor& nf_out = a[11] == Py_None ? nf : vec(a[11], "n_free_out", at::kInt, k.dev, 1);
     if (B > INT32_MAX) throw Bad(PyExc_ValueError, "too many requests");
+    void* const st = stream_of(a[12], k.dev);
+    const Unlocked u;
     return msa_kv4_slots(k.c, ptr<int32_t>(kv), ptr<int32_t>(fresh), (int32_t)B, ptr<int32_t>(tab), stride, (int32_t)tab.size(1),
                          ptr<int32_t>(free), ptr<int32_t>(nf), ptr<int32_t>(kv_out), ptr<int32_t>(nf_out), ptr<int32_t>(cu),
-                         ptr<int64_t>(sl), ptr<int32_t>(pos), sl.numel(), stream_of(a[12], k.dev));
+                         ptr<int64_t>(sl), ptr<int32_t>(pos), sl.numel(), st);
   });
 }
 
@@ -191,8 +203,10 @@ PyObject* release(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& tab = table(a[4], kv.numel(), k.dev, stride);
     const at::Tensor &free = vec(a[5], "free_pages", at::kInt, k.dev, k.c->n_pages), &nf = vec(a[6], "n_free", at::kInt, k.dev, 1);
     if (kv.numel() > INT32_MAX || ids.numel() > INT32_MAX) throw Bad(PyExc_ValueError, "too many requests");
+    void* const st = stream_of(a[7], k.dev);
+    const Unlocked u;
     return msa_kv4_release(k.c, ptr<int32_t>(ids), (int32_t)ids.numel(), ptr<int32_t>(kv), (int32_t)kv.numel(), ptr<int32_t>(tab),
-                           stride, (int32_t)tab.size(1), ptr<int32_t>(free), ptr<int32_t>(nf), stream_of(a[7], k.dev));
+                           stride, (int32_t)tab.size(1), ptr<int32_t>(free), ptr<int32_t>(nf), st);
   });
 }
 
@@ -206,6 +220,7 @@ PyObject* rows_at(PyObject*, PyObject* const* a, Py_ssize_t n) {
     msa_strides s{};
     s.k_head = K.stride(0), s.k_row = K.stride(1), s.v_head = V.stride(0), s.v_row = V.stride(1);
     void* const st = stream_of(a[5], k.dev);
+    const Unlocked u;
     return WRITE ? msa_kv4_append(k.c, K.data_ptr(), V.data_ptr(), &s, ptr<int64_t>(sl), sl.numel(), st)
                  : msa_kv4_read(k.c, K.data_ptr(), V.data_ptr(), &s, ptr<int64_t>(sl), sl.numel(), st);
   });
@@ -233,9 +248,13 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (B > INT32_MAX || Q.size(0) > INT32_MAX || Q.size(1) > INT32_MAX) throw Bad(PyExc_ValueError, "too many rows");
     msa_strides s{};
     s.q_head = Q.stride(0), s.q_row = Q.stride(1), s.o_head = O.stride(0), s.o_row = O.stride(1);
-    return msa_kv4_attend(k.c, Q.data_ptr(), O.data_ptr(), &s, (int32_t)Q.size(1), (int32_t)Q.size(0), (float)number(a[8], "scale"),
+    const float scale = (float)number(a[8], "scale");
+    const int max_q = whole(a[7], "max_q");
+    void* const st = stream_of(a[11], k.dev);
+    const Unlocked u;
+    return msa_kv4_attend(k.c, Q.data_ptr(), O.data_ptr(), &s, (int32_t)Q.size(1), (int32_t)Q.size(0), scale,
                           ptr<int32_t>(tab), stride, (int32_t)tab.size(1), ptr<int32_t>(kv), ptr<int32_t>(cu), (int32_t)B,
-                          whole(a[7], "max_q"), lse, ws.data_ptr(), (size_t)ws.numel(), stream_of(a[11], k.dev));
+                          max_q, lse, ws.data_ptr(), (size_t)ws.numel(), st);
   });
 }
 
@@ -243,7 +262,9 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* status(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 3, [&] {
     const Cache k(a);
-    return msa_kv4_status(k.c, stream_of(a[2], k.dev));
+    void* const st = stream_of(a[2], k.dev);
+    const Unlocked u;
+    return msa_kv4_status(k.c, st);
   });
 }
 
