@@ -66,6 +66,9 @@ const at::Tensor& rows(PyObject* o, const char* name, int64_t heads, int64_t tok
   return t;
 }
 
+// A tensor's stride along an axis.  That of an axis of one says nothing (a tensor that came through DLPack has 1 there).
+int64_t step(const at::Tensor& t, int64_t axis) { return t.size(axis) > 1 ? t.stride(axis) : 0; }
+
 // block table [B, blocks] with contiguous rows
 const at::Tensor& table(PyObject* o, int64_t B, int dev, int64_t& stride) {
   const at::Tensor& t = tensor(o, "block_table");
@@ -158,8 +161,8 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* wk = a[8] == Py_None ? nullptr : vec(a[8], "wk", at::kBFloat16, dev, 128).data_ptr();
     if (Q.size(0) > INT32_MAX || K.size(0) > INT32_MAX) throw Bad(PyExc_ValueError, "too many heads");
     msa_strides in{}, out{};
-    in.q_head = Q.stride(0), in.q_row = Q.stride(1), in.k_head = K.stride(0), in.k_row = K.stride(1);
-    out.q_head = Qo.stride(0), out.q_row = Qo.stride(1), out.k_head = Ko.stride(0), out.k_row = Ko.stride(1);
+    in.q_head = step(Q, 0), in.q_row = step(Q, 1), in.k_head = step(K, 0), in.k_row = step(K, 1);
+    out.q_head = step(Qo, 0), out.q_row = step(Qo, 1), out.k_head = step(Ko, 0), out.k_row = step(Ko, 1);
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
     const float eps = (float)number(a[9], "eps");
     const msa_rope rope = *static_cast<const msa_rope*>(address(a[5]));
@@ -218,7 +221,7 @@ PyObject* rows_at(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& sl = vec(a[4], "slots", at::kLong, k.dev);
     const at::Tensor &K = rows(a[2], "K", k.c->Hkv, sl.numel(), k.dev), &V = rows(a[3], "V", k.c->Hkv, sl.numel(), k.dev);
     msa_strides s{};
-    s.k_head = K.stride(0), s.k_row = K.stride(1), s.v_head = V.stride(0), s.v_row = V.stride(1);
+    s.k_head = step(K, 0), s.k_row = step(K, 1), s.v_head = step(V, 0), s.v_row = step(V, 1);
     void* const st = stream_of(a[5], k.dev);
     const Unlocked u;
     return WRITE ? msa_kv4_append(k.c, K.data_ptr(), V.data_ptr(), &s, ptr<int64_t>(sl), sl.numel(), st)
@@ -247,7 +250,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     if (B > INT32_MAX || Q.size(0) > INT32_MAX || Q.size(1) > INT32_MAX) throw Bad(PyExc_ValueError, "too many rows");
     msa_strides s{};
-    s.q_head = Q.stride(0), s.q_row = Q.stride(1), s.o_head = O.stride(0), s.o_row = O.stride(1);
+    s.q_head = step(Q, 0), s.q_row = step(Q, 1), s.o_head = step(O, 0), s.o_row = step(O, 1);
     const float scale = (float)number(a[8], "scale");
     const int max_q = whole(a[7], "max_q");
     void* const st = stream_of(a[11], k.dev);

@@ -1,0 +1,36 @@
+"""Tensors of unusual strides at the calls around the layer."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+import dynamic_sparse_attention_head_b200 as msa  # noqa: E402
+
+I32, BF16 = torch.int32, torch.bfloat16
+
+
+def _odd(x):
+    """The same tensor with a stride of 1 along its axes of one, as DLPack hands it over."""
+    return x.as_strided(x.shape, [s if n > 1 else 1 for n, s in zip(x.shape, x.stride())], x.storage_offset())
+
+
+@pytest.mark.parametrize("H,T", [(1, 1), (4, 1), (1, 5), (4, 5)])
+def test_strides_of_axes_of_one_are_not_looked_at(H, T):
+    g = torch.Generator(device="cuda").manual_seed(H + T)
+    q, k, v = (torch.randn(H, T, 128, generator=g, device="cuda").to(BF16) for _ in range(3))
+    pos, rope = torch.arange(T, dtype=I32, device="cuda"), msa.Rope()
+    cache, slots = msa.KV4Cache.alloc(2, H, 16, 64), torch.arange(T, device="cuda")
+    table, lens = torch.zeros(1, 1, dtype=I32, device="cuda"), torch.tensor([T], dtype=I32, device="cuda")
+    cu, ws, outs = torch.tensor([0, T], dtype=I32, device="cuda"), cache.alloc_workspace(), []
+    for f in (lambda x: x, _odd):
+        qo, ko, o, kr, vr = (torch.zeros_like(q) for _ in range(5))
+        msa.qk_norm_rope(f(q), f(k), f(qo), f(ko), pos, rope)
+        cache.append(f(ko), f(v), slots)
+        cache.read(slots, f(kr), f(vr))
+        cache.attend(f(qo), f(o), f(table), lens, cu, T, 0.1, ws)
+        outs.append((qo, ko, kr, vr, o))
+    assert cache.device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(*outs)) and outs[1][4].abs().amin(-1).gt(0).any()
