@@ -66,6 +66,14 @@ const at::Tensor& rows(PyObject* o, const char* name, int64_t heads, int64_t tok
   return t;
 }
 
+// The same, written to: rows that share elements (an expanded tensor) would be written over one another.
+const at::Tensor& rows_out(PyObject* o, const char* name, int64_t heads, int64_t tokens, int dev) {
+  const at::Tensor& t = rows(o, name, heads, tokens, dev);
+  for (int axis = 0; axis < 2; ++axis)
+    if (t.size(axis) > 1 && t.stride(axis) < 128 && t.numel()) refuse(name, t, "a tensor whose rows do not overlap" + on(dev));
+  return t;
+}
+
 // A tensor's stride along an axis.  That of an axis of one says nothing (a tensor that came through DLPack has 1 there).
 int64_t step(const at::Tensor& t, int64_t axis) { return t.size(axis) > 1 ? t.stride(axis) : 0; }
 
@@ -152,7 +160,7 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int dev = first.get_device();
     const at::Tensor &Q = rows(a[0], "Q", -1, -1, dev), &K = rows(a[1], "K", -1, Q.size(1), dev);
     const int64_t T = Q.size(1), axes = whole(a[6], "axes");
-    const at::Tensor &Qo = rows(a[2], "Qo", Q.size(0), T, dev), &Ko = rows(a[3], "Ko", K.size(0), T, dev);
+    const at::Tensor &Qo = rows_out(a[2], "Qo", Q.size(0), T, dev), &Ko = rows_out(a[3], "Ko", K.size(0), T, dev);
     const at::Tensor& pos = tensor(a[4], "positions");
     if (!there(pos, at::kInt, pos.dim() == 2 ? 2 : 1, dev) || pos.size(-1) != T || (pos.dim() == 2 ? pos.size(0) : 1) != axes ||
         (T > 1 && pos.stride(-1) != 1))
@@ -219,7 +227,8 @@ PyObject* rows_at(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 6, [&] {
     const Cache k(a);
     const at::Tensor& sl = vec(a[4], "slots", at::kLong, k.dev);
-    const at::Tensor &K = rows(a[2], "K", k.c->Hkv, sl.numel(), k.dev), &V = rows(a[3], "V", k.c->Hkv, sl.numel(), k.dev);
+    constexpr auto rows_of = WRITE ? rows : rows_out;  // an append reads K and V
+    const at::Tensor &K = rows_of(a[2], "K", k.c->Hkv, sl.numel(), k.dev), &V = rows_of(a[3], "V", k.c->Hkv, sl.numel(), k.dev);
     msa_strides s{};
     s.k_head = step(K, 0), s.k_row = step(K, 1), s.v_head = step(V, 0), s.v_row = step(V, 1);
     void* const st = stream_of(a[5], k.dev);
@@ -234,7 +243,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 12, [&] {
     const Cache k(a);
     const at::Tensor& Q = rows(a[2], "Q", -1, -1, k.dev);
-    const at::Tensor& O = rows(a[3], "O", Q.size(0), Q.size(1), k.dev);
+    const at::Tensor& O = rows_out(a[3], "O", Q.size(0), Q.size(1), k.dev);
     const at::Tensor& kv = vec(a[5], "kv_lens", at::kInt, k.dev);
     const int64_t B = kv.numel();
     int64_t stride;

@@ -34,3 +34,28 @@ def test_strides_of_axes_of_one_are_not_looked_at(H, T):
         outs.append((qo, ko, kr, vr, o))
     assert cache.device_status() == 0
     assert all(torch.equal(a, b) for a, b in zip(*outs)) and outs[1][4].abs().amin(-1).gt(0).any()
+
+
+def test_outputs_whose_rows_overlap_are_refused():
+    H, T = 3, 4
+    x = torch.ones(H, T, 128, dtype=BF16, device="cuda")
+    one_head, one_row = x[:1].expand(H, T, 128), x[:, :1].expand(H, T, 128)
+    shifted = torch.ones(1000, dtype=BF16, device="cuda").as_strided((H, T, 128), (200, 64, 1))
+    pos, rope = torch.arange(T, dtype=I32, device="cuda"), msa.Rope()
+    cache, slots = msa.KV4Cache.alloc(2, H, 16, 64), torch.arange(T, device="cuda")
+    table, lens = torch.zeros(1, 1, dtype=I32, device="cuda"), torch.tensor([T], dtype=I32, device="cuda")
+    cu, ws = torch.tensor([0, T], dtype=I32, device="cuda"), cache.alloc_workspace()
+    for y in (one_head, one_row, shifted):
+        for call in (lambda: msa.qk_norm_rope(x, x, y, x.clone(), pos, rope), lambda: msa.qk_norm_rope(x, x, x.clone(), y, pos, rope),
+                     lambda: cache.read(slots, y, x), lambda: cache.read(slots, x, y),
+                     lambda: cache.attend(x, y, table, lens, cu, T, 0.1, ws)):
+            with pytest.raises(ValueError, match="overlap"):
+                call()
+    assert (x == 1).all() and (shifted == 1).all()
+    # as inputs they are as good as any other
+    out = [torch.empty_like(x) for _ in range(2)]
+    cache.append(one_head, one_row, slots)
+    cache.attend(one_row, out[0], table, lens, cu, T, 0.1, ws)
+    cache.append(x, x, slots)
+    cache.attend(x, out[1], table, lens, cu, T, 0.1, ws)
+    assert torch.equal(*out) and cache.device_status() == 0
