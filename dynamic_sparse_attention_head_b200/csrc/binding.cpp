@@ -161,10 +161,17 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor &Q = rows(a[0], "Q", -1, -1, dev), &K = rows(a[1], "K", -1, Q.size(1), dev);
     const int64_t T = Q.size(1), axes = whole(a[6], "axes");
     const at::Tensor &Qo = rows_out(a[2], "Qo", Q.size(0), T, dev), &Ko = rows_out(a[3], "Ko", K.size(0), T, dev);
-    const at::Tensor& pos = tensor(a[4], "positions");
-    if (!there(pos, at::kInt, pos.dim() == 2 ? 2 : 1, dev) || pos.size(-1) != T || (pos.dim() == 2 ? pos.size(0) : 1) != axes ||
-        (T > 1 && pos.stride(-1) != 1))
-      refuse("positions", pos, "int32 [" + std::to_string(axes) + ", " + std::to_string(T) + "] with contiguous rows" + on(dev));
+    const msa_rope rope = *static_cast<const msa_rope*>(address(a[5]));
+    const int32_t* positions = nullptr;  // a norm alone has none
+    int64_t pos_stride = T;
+    if (rope.dim || a[4] != Py_None) {
+      const at::Tensor& pos = tensor(a[4], "positions");
+      if (!there(pos, at::kInt, pos.dim() == 2 ? 2 : 1, dev) || pos.size(-1) != T || (pos.dim() == 2 ? pos.size(0) : 1) != axes ||
+          (T > 1 && pos.stride(-1) != 1))
+        refuse("positions", pos, "int32 [" + std::to_string(axes) + ", " + std::to_string(T) + "] with contiguous rows" + on(dev));
+      positions = ptr<const int32_t>(pos);
+      if (pos.dim() == 2) pos_stride = pos.stride(0);
+    }
     const void* wq = a[7] == Py_None ? nullptr : vec(a[7], "wq", at::kBFloat16, dev, 128).data_ptr();
     const void* wk = a[8] == Py_None ? nullptr : vec(a[8], "wk", at::kBFloat16, dev, 128).data_ptr();
     if (Q.size(0) > INT32_MAX || K.size(0) > INT32_MAX) throw Bad(PyExc_ValueError, "too many heads");
@@ -173,12 +180,10 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     out.q_head = step(Qo, 0), out.q_row = step(Qo, 1), out.k_head = step(Ko, 0), out.k_row = step(Ko, 1);
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
     const float eps = (float)number(a[9], "eps");
-    const msa_rope rope = *static_cast<const msa_rope*>(address(a[5]));
     void* const st = stream_of(a[10], dev);
     const Unlocked u;
     return msa_qk_norm_rope(Q.data_ptr(), K.data_ptr(), &in, Qo.data_ptr(), Ko.data_ptr(), &out, T, (int32_t)Q.size(0),
-                            (int32_t)K.size(0), wq, wk, eps, &rope, ptr<const int32_t>(pos),
-                            pos.dim() == 2 ? pos.stride(0) : T, st);
+                            (int32_t)K.size(0), wq, wk, eps, &rope, positions, pos_stride, st);
   });
 }
 

@@ -53,7 +53,7 @@ def qk_norm_rope(Q, K, Qo, Ko, positions, rope: Rope, wq=None, wk=None, eps: flo
     the rotation at `positions`, in one pass.  Q, Qo [Hq, T, 128], K, Ko [Hkv, T, 128]: bf16 CUDA
     tensors, any head and token strides that are multiples of 8 (the projection's [T, H, 128]
     transposed); Qo / Ko may be Q / K.  positions: int32 [T], or [axes, T] for a rope with sections
-    (expanded from one row where the axes agree)."""
+    (expanded from one row where the axes agree); None for a norm alone (dim = 0)."""
     code = _native.norm_rope(Q, K, Qo, Ko, positions, ctypes.addressof(rope._c), rope.n_axes, wq, wk, eps,
                              None if stream is None else stream.cuda_stream)
     if code:

@@ -59,3 +59,20 @@ def test_outputs_whose_rows_overlap_are_refused():
     cache.append(x, x, slots)
     cache.attend(x, out[1], table, lens, cu, T, 0.1, ws)
     assert torch.equal(*out) and cache.device_status() == 0
+
+
+def test_a_norm_alone_needs_no_positions():
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k = (torch.randn(h, 9, 128, generator=g, device="cuda").to(BF16) for h in (3, 2))
+    w = [torch.randn(128, generator=g, device="cuda").to(BF16) for _ in range(2)]
+    outs = []
+    for pos in (torch.arange(9, dtype=I32, device="cuda"), None):
+        qo, ko = torch.empty_like(q), torch.empty_like(k)
+        msa.qk_norm_rope(q, k, qo, ko, pos, msa.Rope(dim=0), *w)
+        outs.append((qo, ko))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    x = q.double() * torch.rsqrt(q.double().square().mean(-1, keepdim=True) + 1e-6) * w[0].double()
+    # one rounding to bf16, and fp32's before it (a sum of 128 squares, rsqrt, two products: below 2^-20)
+    assert ((outs[1][0].double() - x).abs() <= x.abs() * (2.0 ** -8 + 2.0 ** -18)).all()
+    with pytest.raises(TypeError):
+        msa.qk_norm_rope(q, k, *outs[0], None, msa.Rope(dim=16))
