@@ -89,8 +89,8 @@ struct SlotArgs {
 // share of the tokens and of the new pages by a search in the two running sums; nothing is passed
 // between blocks.  kv_lens_out and n_free_out may be the inputs: they are written by the block
 // that arrives last, when every block has read them.  Bound by launch latency for a decode batch (256
-// requests: 4.2 us in a graph, 5.2 with a scan for each sum); for prompts by the searches behind the 12 bytes
-// written per token (0.73 M tokens of 7 requests: 8.6 us; 10.2 where every block waited for its arrival's answer).
+// requests: 4.4 us in a graph, 5.2 with a scan for each sum); for prompts by the searches behind the 12 bytes
+// written per token (0.73 M tokens of 7 requests: 8.8 us; 10.2 where every block waited for its arrival's answer).
 __global__ void __launch_bounds__(SLOT_THREADS) kv4_slots_kernel(const SlotArgs a) {
   extern __shared__ int32_t sm[];
   int32_t* cum_new = sm;                      // [B + 1]
@@ -474,7 +474,7 @@ __device__ __forceinline__ uint4 dequantise8(uint32_t code, uint32_t scale_word)
 }
 
 // Bound by HBM and, nearly, by issue (78 %): the append's bytes the other way round.  262144 tokens, 4 heads, groups
-// of 128: 123 to 128 us, 5.4 TB/s; with one row in flight 147 us.
+// of 128: 123 to 129 us, 5.4 TB/s; with one row in flight 147 us.
 template <int NG>
 __global__ void __launch_bounds__(ROW_THREADS) kv4_read_kernel(const RowArgs a) {
   using Blk = Kv4Block<NG>;

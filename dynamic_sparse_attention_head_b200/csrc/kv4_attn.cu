@@ -26,8 +26,8 @@
 // bandwidth.
 //
 // Floor for long contexts: HBM, 2 (64 + 4 NG) bytes per key and KV head.  Measured: 64 requests of up to 16384
-// tokens, 32 / 8 heads, groups of 128: 118 to 125 us, 4.6 TB/s (a copy: 6.44); one token over 1048576, 28 / 4 heads,
-// groups of 64: 129 to 135 us, the same rate; 4 requests of up to 700 tokens: 12.3 us.  Bound by the issue of 12 warps an SM (57 to
+// tokens, 32 / 8 heads, groups of 128: 122 to 126 us, 4.5 TB/s (a copy: 6.44); one token over 1048576, 28 / 4 heads,
+// groups of 64: 134 to 136 us, the same rate; 4 requests of up to 700 tokens: 12.3 us.  Bound by the issue of 12 warps an SM (57 to
 // 60 %, ALU 56 %: 259 instructions per 16 keys, half of them to take the codes apart) and, for 11 % of the
 // time, by the start and the joins.
 #include <cuda_bf16.h>
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(W * 32, 1) kv4_attend_kernel(const __grid_cons
               for (int e = 0; e < 2; ++e) {
                 // a key hidden from this row alone may hold NaN: no product with it
                 const bool hidden = PARTIAL && key >= lim[nt][e];
-                y[e] = hidden ? 0.f : p[nt][e] * vs;
+                y[e] = hidden ? 0.f : p[nt][e] * vs;  // to fp16: up to 2^15, and 2^-25 lost of small ones
                 z[gr][nt][e] = hidden ? z[gr][nt][e] : fmaf(p[nt][e], vz, z[gr][nt][e]);
               }
               pf[gr][nt][r] = transpose8x8(half2_bits(y[0], y[1]));

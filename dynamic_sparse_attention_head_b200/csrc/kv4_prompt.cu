@@ -21,8 +21,8 @@
 // come in equal folds on one line, of which every CTA takes an equal stretch.  A pair cut by a stretch's
 // border leaves fp32 rows in the workspace; a second small kernel joins them in a fixed order.
 //
-// Measured (follow-up prompts of 601 and 316 tokens over 32768 and 10732 cached ones, 28 / 4 heads): 538 us, 610
-// TFLOP/s.  A pair of tiles takes 4700 to 6000 cycles.  The tensor pipe needs 2176 of them, the exponentials
+// Measured (follow-up prompts of 601 and 316 tokens over 32768 and 10732 cached ones, 28 / 4 heads): 521 us, 630
+// TFLOP/s.  (The split below was taken at 538 us.)  A pair of tiles takes 4700 to 6000 cycles.  The tensor pipe needs 2176 of them, the exponentials
 // 2048, shared memory about 2550 (147 KB of Q K operands, 64 KB of P V's, 115 KB around the widening); the
 // chain through them is what counts: widening 2700 (keys) and 1150 (values), products 1750 under that
 // contention, softmax 2440.  Moving the scales' share of the widening to a warp of its own shortened the first
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv4_prompt_kernel(const __grid_con
                   e.x *= pow2(-(int)(ct.key_down[kt & 3][32 * h + 2 * c] >> 4));
                   e.y *= pow2(-(int)(ct.key_down[kt & 3][32 * h + 2 * c + 1] >> 4));
                 }
-                pk[c] = half2_bits(e.x, e.y);
+                pk[c] = half2_bits(e.x, e.y);  // 11 bits: O is rounded to 8
               }
               tmem_st16(s_own + 16 * h, pk);
             }

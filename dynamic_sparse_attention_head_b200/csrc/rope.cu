@@ -11,7 +11,7 @@
 // Sixteen lanes hold one row, 8 channels (16 bytes) each.  They take the cosines of one token once
 // and then walk over a run of its heads, four rows in flight, so the 8 sincospif of a lane are
 // shared by the run.  Bound by HBM: 512 bytes a row, read and written once.  131072 tokens, 28 + 4 heads,
-// three axes: 387 to 394 us, 5.5 TB/s (a copy: 6.44); with the norm before the rotation, partners exchanged as
+// three axes: 387 to 397 us, 5.5 TB/s (a copy: 6.44); with the norm before the rotation, partners exchanged as
 // fp32, 471 us (issue-bound).
 #include <cuda_bf16.h>
 #include <math.h>

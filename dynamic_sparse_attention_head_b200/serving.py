@@ -134,7 +134,8 @@ class KV4Cache:
     def attend(self, Q, O, block_table, kv_lens, cu_q, max_q: int, scale: float, ws, lse=None, stream=None):
         """msa_kv4_attend: Q, O [Hq, T, 128] (bf16); request b's query tokens are columns cu_q[b] ..
         cu_q[b + 1) and the last of its kv_lens[b] cached tokens.  max_q: the most query tokens of any
-        request (picks the kernel's tile).  lse: fp32 [Hq, T] or None.  ws: alloc_workspace()."""
+        request (picks the kernel for all requests of the call: long prompts and single tokens are better served
+        by a call each).  lse: fp32 [Hq, T] or None.  ws: alloc_workspace()."""
         code = _native.attend(self._addr, self._dev, Q, O, block_table, kv_lens, cu_q, max_q, scale, ws, lse,
                               None if stream is None else stream.cuda_stream)
         if code:

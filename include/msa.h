@@ -451,13 +451,22 @@ msa_status msa_kv4_read(const msa_kv4_cache* cache, void* K, void* V, const msa_
  * stands for (bf16; O may be Q itself, with its strides), lse (optional, fp32 [Hq][total_q]) the natural-log normaliser.  A row that sees
  * no key has O = 0 and lse = -inf.  Rows behind cu_q[B] are left as they were.  Query head h reads KV
  * head h / (Hq / Hkv).  Any number of query tokens per request (one each: decoding; a few: draft
- * verification; many: a prompt over a cached prefix); max_q, the most of any request, picks the
- * kernel's tile and nothing else.  Page numbers outside the cache hide their keys, lengths outside
- * the table row or Q are cut, and both are recorded as an error.  scale > 0.  B <= 2048, a row of the table
+ * verification; many: a prompt over a cached prefix).  max_q, the most of any request, and the width of the table
+ * pick one kernel for all requests of the call: the one for many rows from max_q * Hq / Hkv = 80 on (512 where the
+ * table's rows hold less than 1024 tokens).  The choice changes cost and rounding, not what a row sees, whatever the
+ * requests then hold.  Single tokens beside a long prompt cost several times what they cost alone: give the prompts a
+ * call of their own, and tables cut to the lengths.  Page numbers outside the cache hide their keys, lengths outside
+ * the table row or Q are cut, and both are recorded as an error; so is a call of 2^31 tiles and more (of 8 query rows
+ * of a KV head by 16 keys, at the least), which writes nothing.  scale > 0.  B <= 2048, a row of the table
  * holds at most 2^31 - 2^16 tokens.
  * ws: device, 256-byte aligned, msa_kv4_attend_workspace_bytes() bytes, zero-filled once by the
  * caller; every call leaves it ready for the next, of any shape.  Calls that may overlap on the GPU
- * need a workspace each.  Sums in fp32 and in a fixed order: the same inputs give the same bits. */
+ * need a workspace each.
+ * Precision: scores, softmax and all sums in fp32, in a fixed order (the same inputs give the same bits).  The second
+ * product takes its weights (few rows: times the values' step; many rows: the values too) rounded to fp16, 2^-11 of each;
+ * what a weight loses where it is small is below 2^-32 of the row's largest (few rows: of that times the largest step
+ * over the value's own), while the normaliser keeps all of it.  Keys and values of one token 2^20 times the others'
+ * leave these their own precision (many rows: the weights of the up to 127 other keys of its tile lose that much more). */
 size_t msa_kv4_attend_workspace_bytes(void);
 msa_status msa_kv4_attend(const msa_kv4_cache* cache, const void* Q, void* O, const msa_strides* strides,
                           int32_t total_q, int32_t Hq, float scale, const int32_t* block_table, int64_t table_stride,
